@@ -20,7 +20,10 @@ __all__ = ["GdnError", "lib", "library_path", "STATUS", "VARIANTS", "check_error
            "chunk_fwd_workspace_bytes", "chunk_fwd_launches", "decode_step", "decode_layer_step",
            "gates", "gates_bwd", "prologue", "out_norm", "layer_fwd", "layer_fwd_varlen",
            "layer_fwd_static", "layer_workspace_bytes", "bwd", "bwd_varlen", "bwd_workspace_bytes",
-           "bwd_launches", "layer_bwd", "layer_bwd_varlen", "layer_bwd_workspace_bytes"]
+           "bwd_launches", "layer_bwd", "layer_bwd_varlen", "layer_bwd_workspace_bytes",
+           "ssm_conv", "ssm_conv_varlen", "ssm_scan", "ssm_scan_varlen",
+           "ssm_scan_workspace_bytes", "ssm_step", "block_norm", "block_norm_bwd",
+           "block_norm_bwd_workspace_bytes"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libgdn.so")
@@ -122,6 +125,21 @@ def lib() -> ctypes.CDLL:
         L.gdn_layer_bwd_varlen_workspace_bytes.restype = SZ
         L.gdn_gates_bwd.argtypes = [P, P, P, P, LL, I, I, P]
         L.gdn_gates_bwd.restype = I
+        L.gdn_ssm_conv.argtypes = [P, LL] + [P] * 5 + [I] * 4 + [P]
+        L.gdn_ssm_conv_varlen.argtypes = [P, LL] + [P] * 3 + [I, I] + [P] * 3 + [I] * 3 + [P]
+        L.gdn_ssm_scan.argtypes = [P, LL] * 5 + [P] * 7 + [SZ] + [I] * 7 + [P]
+        L.gdn_ssm_scan_varlen.argtypes = [P, LL] * 5 + [P] * 4 + [I, I] + [P] * 4 + [SZ] + \
+            [I] * 6 + [P]
+        L.gdn_ssm_step.argtypes = [P, LL] * 3 + [P] * 9 + [I] * 6 + [P]
+        L.gdn_block_norm.argtypes = [P] * 8 + [LL, I, F, I, I, P]
+        L.gdn_block_norm_bwd.argtypes = [P] * 15 + [SZ, LL, I, F, I, I, P]
+        for fn in (L.gdn_ssm_conv, L.gdn_ssm_conv_varlen, L.gdn_ssm_scan, L.gdn_ssm_scan_varlen,
+                   L.gdn_ssm_step, L.gdn_block_norm, L.gdn_block_norm_bwd):
+            fn.restype = I
+        L.gdn_ssm_scan_workspace_bytes.argtypes = [I] * 7
+        L.gdn_ssm_scan_workspace_bytes.restype = SZ
+        L.gdn_block_norm_bwd_workspace_bytes.argtypes = [LL, I]
+        L.gdn_block_norm_bwd_workspace_bytes.restype = SZ
         _lib = L
     return _lib
 
@@ -680,3 +698,280 @@ def check_error(device: Optional[torch.device] = None):
     dev = device or torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(dev):
         _check("gdn_check_error", lib().gdn_check_error(_stream(dev)))
+
+
+# ------------------------------------------------------------------------------------------------
+# selective state space block
+# ------------------------------------------------------------------------------------------------
+def _cuda(*ts: Optional[torch.Tensor]) -> torch.device:
+    """The one CUDA device of the tensors (any layout)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("all tensors must be on one device")
+    return dev
+
+
+def _dense(*ts: Optional[torch.Tensor]):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("states, histories, weights and offsets must be contiguous")
+
+
+def _row_ld(t: Optional[torch.Tensor], lead: int, name: str) -> int:
+    """Values between two tokens of ``t`` [tokens..., inner...] (``lead`` token dimensions), whose
+    tokens are evenly spaced and whose inner dimensions lie without gaps: a slice of the columns of
+    a contiguous tensor, or a contiguous tensor."""
+    if t is None:
+        return 0
+    want = 1
+    for i in range(t.dim() - 1, lead - 1, -1):
+        if t.shape[i] > 1 and t.stride(i) != want:
+            raise ValueError(f"{name}: the values of a token must be contiguous")
+        want *= t.shape[i]
+    ld, span = max(want, 1), None
+    for i in range(lead - 1, -1, -1):
+        if t.shape[i] > 1:
+            if span is None:
+                ld = span = t.stride(i)
+            elif t.stride(i) != span:
+                raise ValueError(f"{name}: the tokens must be evenly spaced")
+        if span is not None:
+            span *= t.shape[i]
+    if ld < want:
+        raise ValueError(f"{name}: the tokens overlap")
+    return ld
+
+
+def _call(name: str, dev: torch.device, *args):
+    """Call the library on ``dev``'s current stream (made current where it is not)."""
+    fn = getattr(lib(), name)
+    stream = _stream(dev)
+    if torch.cuda.current_device() == dev.index:
+        _check(name, fn(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, fn(*args, stream))
+
+
+def _conv(x, lead, w, bias, hist, nseq, want_hist, out):
+    C = x.shape[-1]
+    if w.shape != (C, 4) or (bias is not None and bias.shape != (C,)):
+        raise ValueError("w must be [C, 4] and bias [C]")
+    if hist is not None and (hist.shape != (nseq, 3, C) or hist.dtype != x.dtype):
+        raise ValueError("hist must be [sequences, 3, C] in x's dtype")
+    if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
+        raise ValueError("out must have x's shape and dtype")
+    _f32(w, bias)
+    io = _io_dtype(x)
+    _dense(w, bias, hist, out)
+    ld = _row_ld(x, lead, "x")
+    if out is None:
+        out = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+    hist_out = torch.empty(nseq, 3, C, device=x.device, dtype=x.dtype) if want_hist else None
+    return out, hist_out, ld, io, _cuda(x, w, bias, hist, out)
+
+
+def ssm_conv(x, w, bias=None, *, hist=None, want_hist: bool = False,
+             out: Optional[torch.Tensor] = None):
+    """Short causal convolution of the state space block, then SiLU: x [B,T,C] (a slice of a wider
+    row may be given), w [C,4] (tap 3 on the current token), bias [C] or None, ``hist`` [B,3,C] the
+    raw rows before (None: zeros).  Returns out [B,T,C], or (out, hist_out) with ``want_hist``."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    B, T, C = x.shape
+    out, hist_out, ld, io, dev = _conv(x, 2, w, bias, hist, B, want_hist, out)
+    _call("gdn_ssm_conv", dev, _p(x), ld, _p(w), _p(bias), _p(hist), _p(out), _p(hist_out), B, T, C,
+          io)
+    return (out, hist_out) if want_hist else out
+
+
+def ssm_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, *, hist=None, want_hist: bool = False,
+                    out: Optional[torch.Tensor] = None):
+    """``ssm_conv`` over packed sequences: x [total,C], cu_seqlens [nseq+1] int32 (device), hist
+    [nseq,3,C].  Rows in no sequence keep their ``out``."""
+    if x.dim() != 2:
+        raise ValueError("x must be [total, C]")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32 [nseq + 1]")
+    nseq = cu_seqlens.numel() - 1
+    out, hist_out, ld, io, dev = _conv(x, 1, w, bias, hist, nseq, want_hist, out)
+    _cuda(x, cu_seqlens)
+    _call("gdn_ssm_conv_varlen", dev, _p(x), ld, _p(w), _p(bias), _p(cu_seqlens), nseq,
+          int(max_seqlen), _p(hist), _p(out), _p(hist_out), x.shape[0], x.shape[1], io)
+    return (out, hist_out) if want_hist else out
+
+
+def ssm_scan_workspace_bytes(nseq, max_seqlen, H, G, P, N, dtype) -> int:
+    """Device scratch bytes ``ssm_scan`` / ``ssm_scan_varlen`` need (0: none)."""
+    return int(lib().gdn_ssm_scan_workspace_bytes(nseq, max_seqlen, H, G, P, N, _DTYPES[dtype]))
+
+
+def _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, lead, nseq, max_len, want_state, out, state_out,
+          workspace):
+    H, P = x.shape[lead:]
+    tok = tuple(x.shape[:lead])
+    if dt.shape != tok + (H,) or Bm.dim() != lead + 2 or tuple(Bm.shape[:lead]) != tok \
+            or Cm.shape != Bm.shape or (z is not None and z.shape != x.shape):
+        raise ValueError("x, dt, Bm, Cm, z shapes disagree")
+    G, N = Bm.shape[lead:]
+    for t in (dt, Bm, Cm, z):
+        if t is not None and t.dtype != x.dtype:
+            raise ValueError("x, dt, Bm, Cm, z must have one dtype")
+    for t in (A_log, D, dt_bias):
+        if t is not None and t.shape != (H,):
+            raise ValueError("A_log, D, dt_bias must be [H]")
+    for t in (S0, state_out):
+        if t is not None and t.shape != (nseq, H, N, P):
+            raise ValueError("states must be [sequences, H, N, P]")
+    if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
+        raise ValueError("out must have x's shape and dtype")
+    _f32(A_log, D, dt_bias, S0, state_out)
+    io = _io_dtype(x)
+    _dense(A_log, D, dt_bias, S0, state_out, out, workspace)
+    y = torch.empty(x.shape, device=x.device, dtype=x.dtype) if out is None else out
+    sT = state_out
+    if sT is None and want_state:
+        sT = torch.empty(nseq, H, N, P, device=x.device, dtype=torch.float32)
+    dev = _cuda(x, dt, Bm, Cm, z, A_log, D, dt_bias, S0, y, sT, workspace)
+    need = int(lib().gdn_ssm_scan_workspace_bytes(nseq, max_len, H, G, P, N, io))
+    ws, wbytes = _workspace(need, dev, workspace)
+    head = (_p(x), _row_ld(x, lead, "x"), _p(dt), _row_ld(dt, lead, "dt"), _p(Bm),
+            _row_ld(Bm, lead, "Bm"), _p(Cm), _row_ld(Cm, lead, "Cm"), _p(z), _row_ld(z, lead, "z"),
+            _p(A_log), _p(D), _p(dt_bias))
+    return y, sT, head, (_p(S0), _p(y), _p(sT), _p(ws), wbytes), (H, G, P, N, io), dev
+
+
+def ssm_scan(x, dt, A_log, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None,
+             want_state: bool = True, out: Optional[torch.Tensor] = None,
+             state_out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None
+             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Selective scan over prompts: x [B,T,H,P], dt [B,T,H], Bm, Cm [B,T,G,N], z [B,T,H,P] or None
+    in one dtype (column slices of wider rows may be given); A_log, D, dt_bias [H] fp32; S0
+    [B,H,N,P] fp32 or None.  Returns (y [B,T,H,P], S_T [B,H,N,P] or None)."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, P]")
+    B, T = x.shape[:2]
+    y, sT, head, mid, dims, dev = _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, 2, B, T, want_state,
+                                        out, state_out, workspace)
+    _call("gdn_ssm_scan", dev, *head, *mid, B, T, *dims)
+    return y, sT
+
+
+def ssm_scan_varlen(x, dt, A_log, Bm, Cm, cu_seqlens, max_seqlen: int, *, D=None, z=None,
+                    dt_bias=None, S0=None, want_state: bool = True,
+                    out: Optional[torch.Tensor] = None,
+                    state_out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None
+                    ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``ssm_scan`` over packed sequences: [total,...] token tensors, cu_seqlens [nseq+1] int32
+    (device), states [nseq,H,N,P].  Rows in no sequence keep their ``out``."""
+    if x.dim() != 3:
+        raise ValueError("x must be [total, H, P]")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32 [nseq + 1]")
+    nseq, max_seqlen = cu_seqlens.numel() - 1, int(max_seqlen)
+    y, sT, head, mid, dims, dev = _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, 1, nseq, max_seqlen,
+                                        want_state, out, state_out, workspace)
+    _cuda(x, cu_seqlens)
+    _call("gdn_ssm_scan_varlen", dev, *head, _p(cu_seqlens), nseq, max_seqlen, *mid, x.shape[0], *dims)
+    return y, sT
+
+
+def ssm_step(u, dt, hist, w, bias, A_log, S, *, groups: int, D=None, z=None, dt_bias=None,
+             hist_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None
+             ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token of the state space block for n sequences: u [n, H*P + 2*groups*N] raw rows
+    [x | B | C], dt [n,H], z [n,H,P] or None; hist [n,3,H*P + 2*groups*N] raw rows before; w, bias
+    of the convolution; S [n,H,N,P] fp32, updated in place.  Returns (y [n,H,P], hist_out), the
+    history moved on by one token (into ``hist_out`` if given, never into ``hist`` itself)."""
+    if S.dim() != 4 or u.dim() != 2 or groups <= 0:
+        raise ValueError("S must be [n, H, N, P], u [n, channels], groups positive")
+    n, H, N, P = S.shape
+    C = H * P + 2 * groups * N
+    if u.shape != (n, C) or dt.shape != (n, H) or hist.shape != (n, 3, C) or w.shape != (C, 4) \
+            or (bias is not None and bias.shape != (C,)) or (z is not None and z.shape != (n, H, P)):
+        raise ValueError("u, dt, hist, w, bias, z shapes disagree with S and groups")
+    for t in (A_log, D, dt_bias):
+        if t is not None and t.shape != (H,):
+            raise ValueError("A_log, D, dt_bias must be [H]")
+    hist_out = torch.empty(hist.shape, device=hist.device, dtype=hist.dtype) if hist_out is None else hist_out
+    y = torch.empty(n, H, P, device=u.device, dtype=u.dtype) if out is None else out
+    if hist_out.shape != hist.shape or y.shape != (n, H, P):
+        raise ValueError("hist_out or out has another shape")
+    for t in (dt, hist, hist_out, z, y):
+        if t is not None and t.dtype != u.dtype:
+            raise ValueError("u, dt, hist, z and the outputs must have one dtype")
+    _f32(w, bias, A_log, D, dt_bias, S)
+    _dense(hist, hist_out, w, bias, A_log, D, dt_bias, S, y)
+    dev = _cuda(u, dt, hist, w, bias, A_log, S, D, z, dt_bias, hist_out, y)
+    _call("gdn_ssm_step", dev, _p(u), _row_ld(u, 1, "u"), _p(dt), _row_ld(dt, 1, "dt"), _p(z),
+          _row_ld(z, 1, "z"), _p(hist), _p(hist_out), _p(w), _p(bias), _p(A_log), _p(D), _p(dt_bias),
+          _p(S), _p(y), n, H, groups, P, N, _io_dtype(u))
+    return y, hist_out
+
+
+# ------------------------------------------------------------------------------------------------
+# the norms before and after a block
+# ------------------------------------------------------------------------------------------------
+def _norm_args(y, h, z, w_post, w_pre, res_scale):
+    D = y.shape[-1]
+    if h.shape != y.shape or (z is not None and z.shape != y.shape):
+        raise ValueError("y, h and z must have one shape")
+    if z is not None and z.dtype != y.dtype:
+        raise ValueError("y and z must have one dtype")
+    for t in (w_post, w_pre, res_scale):
+        if t is not None and t.shape != (D,):
+            raise ValueError("w_post, w_pre and res_scale must be [D]")
+    _f32(w_post, w_pre, res_scale)
+    return (y.numel() // D if D else 0), D, _io_dtype(y), _io_dtype(h)
+
+
+def block_norm(y, h, *, w_post=None, w_pre=None, z=None, res_scale=None, eps: float = 1e-5
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The residual step around a block: h_out = h + res_scale * SiLU(z) * (RMSNorm(y) * w_post) and
+    the next block's input x = RMSNorm(h_out) * w_pre.  y, z [..., D] in one dtype; h [..., D] in it
+    or in float32; w_post, w_pre, res_scale [D] fp32, each optional.  Returns (h_out, x), x None
+    without ``w_pre``."""
+    rows, D, io, ho = _norm_args(y, h, z, w_post, w_pre, res_scale)
+    dev = _dev(y, h, z, w_post, w_pre, res_scale)
+    h_out = torch.empty(h.shape, device=dev, dtype=h.dtype)
+    x = None if w_pre is None else torch.empty(y.shape, device=dev, dtype=y.dtype)
+    _call("gdn_block_norm", dev, _p(y), _p(h), _p(z), _p(w_post), _p(w_pre), _p(res_scale), _p(h_out),
+          _p(x), rows, D, float(eps), io, ho)
+    return h_out, x
+
+
+def block_norm_bwd_workspace_bytes(rows: int, D: int) -> int:
+    """Device scratch bytes one ``block_norm_bwd`` call needs."""
+    return int(lib().gdn_block_norm_bwd_workspace_bytes(rows, D))
+
+
+def block_norm_bwd(y, h_out, dh_out, dx=None, *, w_post=None, w_pre=None, z=None, res_scale=None,
+                   eps: float = 1e-5, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of <dh_out, h_out> + <dx, x> of ``block_norm`` from its y, its output h_out and z:
+    dict of dy, dh, dz (in their inputs' dtypes) and dw_post, dw_pre, dres_scale (fp32); None for
+    what the call does not have.  dh_out may be None where there is a ``w_pre``."""
+    rows, D, io, ho = _norm_args(y, h_out, z, w_post, w_pre, res_scale)
+    if (dx is None) != (w_pre is None) or (dx is not None and (dx.shape != y.shape or dx.dtype != y.dtype)):
+        raise ValueError("dx comes with w_pre, in y's shape and dtype")
+    if dh_out is None and w_pre is None:
+        raise ValueError("dh_out is needed without w_pre")
+    if dh_out is not None and (dh_out.shape != y.shape or dh_out.dtype != h_out.dtype):
+        raise ValueError("dh_out must have h_out's shape and dtype")
+    dev = _dev(y, h_out, dh_out, dx, z, w_post, w_pre, res_scale, workspace)
+    like = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)
+    g = {"dy": like(y), "dh": like(h_out), "dz": like(z), "dw_post": like(w_post), "dw_pre": like(w_pre),
+         "dres_scale": like(res_scale)}
+    ws, wbytes = _workspace(block_norm_bwd_workspace_bytes(rows, D), dev, workspace)
+    _call("gdn_block_norm_bwd", dev, _p(y), _p(h_out), _p(z), _p(dh_out), _p(dx), _p(w_post), _p(w_pre),
+          _p(res_scale), _p(g["dy"]), _p(g["dh"]), _p(g["dz"]), _p(g["dw_post"]), _p(g["dw_pre"]),
+          _p(g["dres_scale"]), _p(ws), wbytes, rows, D, float(eps), io, ho)
+    return g

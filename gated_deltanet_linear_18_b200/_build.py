@@ -4,6 +4,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,9 +16,10 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
-    "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden", "-shared",
+    "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
     "-Xptxas", "-warn-spills",
 ]
+UNITS = ("gdn_api.cu", "ssm_api.cu", "norm_api.cu")
 
 
 def sources():
@@ -33,15 +35,26 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile csrc/gdn_api.cu (which includes every kernel) into libgdn.so next to this file."""
+    """Compile the units of csrc (side by side) and link them into libgdn.so next to this file."""
     if not force and not stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-o", tmp,
-           os.path.join(CSRC, "gdn_api.cu")]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
+    objs = [f"{tmp}.{u[:-3]}.o" for u in UNITS]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.check_call(cmd)
+
+    try:
+        with ThreadPoolExecutor(len(UNITS)) as pool:
+            list(pool.map(lambda uo: run([NVCC, *FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", "-o", uo[1],
+                                          os.path.join(CSRC, uo[0])]), zip(UNITS, objs)))
+        run([NVCC, *FLAGS, "-shared", "-o", tmp, *objs])
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,4 +1,5 @@
-// Shared device helpers of the gated delta rule library (one translation unit: gdn_api.cu).
+// Shared device helpers of the gated delta rule library.  Each translation unit (gdn_api.cu,
+// ssm_api.cu, norm_api.cu) has an error word of its own; gdn_check_error reads them all.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,8 +9,9 @@
 namespace gdn {
 
 // Per-device error word.  Kernels that give up on a bounded wait OR a bit in here and skip the rest
-// of their work; gdn_check_error reads and clears it.  Statically allocated with the module.
-__device__ unsigned int g_error_word = 0u;
+// of their work; gdn_check_error reads and clears it.  Statically allocated with the module; local
+// to the translation unit.
+static __device__ unsigned int g_error_word = 0u;
 
 enum : unsigned int { kErrTimeout = 1u };
 

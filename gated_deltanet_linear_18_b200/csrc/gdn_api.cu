@@ -1,5 +1,6 @@
 // C ABI of the gated delta rule library (declared in include/gdn.h): argument validation,
-// kernel selection and launches.  All kernels of the library are compiled in this one unit.
+// kernel selection and launches of the gated delta rule's calls (ssm_api.cu and norm_api.cu hold the
+// state space block's and the block norms').
 #include <stdint.h>
 #include <string.h>
 
@@ -17,9 +18,15 @@
 
 using namespace gdn;
 
+namespace gdn {
+// The error words of the other translation units (read and cleared).
+bool ssm_take_error(unsigned int* word);
+bool norm_take_error(unsigned int* word);
+}  // namespace gdn
+
 namespace {
 
-constexpr int kVersion = 10000;   // 1.0.0
+constexpr int kVersion = 10100;   // 1.1.0
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool opt_aligned16(const void* p) { return p == nullptr || aligned16(p); }
@@ -413,7 +420,9 @@ gdn_status gdn_check_error(gdn_stream_t stream) {
   if (cudaMemcpyFromSymbol(&word, g_error_word, sizeof(word)) != cudaSuccess) return GDN_ERR_CUDA;
   if (word != 0 && cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess)
     return GDN_ERR_CUDA;
-  return (word & kErrTimeout) ? GDN_ERR_TIMEOUT : GDN_OK;
+  unsigned int ssm_word = 0, norm_word = 0;
+  if (!ssm_take_error(&ssm_word) || !norm_take_error(&norm_word)) return GDN_ERR_CUDA;
+  return ((word | ssm_word | norm_word) & kErrTimeout) ? GDN_ERR_TIMEOUT : GDN_OK;
 }
 
 size_t gdn_chunk_fwd_varlen_workspace_bytes(int nseq, int max_seqlen, int Hk, int Hv, int dk,

@@ -1,0 +1,29 @@
+// What the state space kernels share: arguments of the scan and the time step's arithmetic.
+#pragma once
+
+#include "common.cuh"
+
+namespace gdn {
+namespace ssm {
+
+// log(1 + e^v) without overflow; the accurate functions: one value per (token, head).
+__device__ __forceinline__ float softplus(float v) {
+  return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
+}
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+
+// One call of the scan.  Token tensors have `ld*` values between tokens; inside a token's row the
+// heads (groups) follow one another without gaps.
+struct ScanArgs {
+  const void *x, *dt, *B, *C, *z;       // [rows, H, P], [rows, H], [rows, G, N] twice, [rows, H, P]
+  long ldx, lddt, ldb, ldc, ldz;
+  const float *A_log, *D, *dt_bias;     // [H]; D, dt_bias may be null
+  const float* S0;                      // [nseq, H, N, P] or null
+  void* y;                              // [rows, H, P], no gaps
+  float* S_T;                           // [nseq, H, N, P] or null
+  const int* cu;                        // null: nseq sequences of T rows
+  int nseq, T, max_len, H, G;
+};
+
+}  // namespace ssm
+}  // namespace gdn

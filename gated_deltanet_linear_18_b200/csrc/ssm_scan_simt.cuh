@@ -1,0 +1,101 @@
+// The selective scan on CUDA cores, token by token, in fp32: every type and shape.
+//   D_t = softplus(dt_t + dt_bias)   S_t = exp(-D_t exp(A_log)) S_{t-1} + D_t B_t x_t^T
+//   y_t = (S_t^T C_t + D x_t) SiLU(z_t)
+//
+// A CTA owns PT = min(P, 32) columns of one (sequence, head): 128 threads as PT columns x NG
+// groups of N / NG state rows, the state in registers.  Tokens come in tiles of kTile through
+// shared memory (B and C as rows that a whole warp reads at one address); the NG partial read-outs
+// of a tile are added at its end.  Bound by the chain of tokens (3 N P operations each, issued by
+// four warps); it is the fp32 path and the one for shapes without a tensor-core kernel.
+#pragma once
+
+#include "ssm_common.cuh"
+
+namespace gdn {
+namespace ssm {
+
+constexpr int kSimtThreads = 128;
+constexpr int kTile = 16;
+
+template <int N, int P, typename T>
+__global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs a) {
+  constexpr int PT = P < 32 ? P : 32;
+  constexpr int NG = kSimtThreads / PT;
+  constexpr int NR = N / NG;
+  static_assert(N % NG == 0, "state rows divide over the groups");
+  const int nblk = P / PT;
+  const int pb = blockIdx.x % nblk, h = blockIdx.x / nblk, seq = blockIdx.y;
+  const int g = h / (a.H / a.G);
+  const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
+  const int tid = threadIdx.x, col = tid % PT, ng = tid / PT;
+  const int p0 = pb * PT;
+
+  __shared__ __align__(16) float sB[kTile][N];
+  __shared__ __align__(16) float sC[kTile][N];
+  __shared__ float sx[kTile][PT];
+  __shared__ float s_step[kTile], s_fade[kTile];
+  __shared__ float part[kTile][NG][PT + 1];
+
+  const T* __restrict__ x = static_cast<const T*>(a.x) + (long)h * P + p0;
+  const T* __restrict__ dt = static_cast<const T*>(a.dt) + h;
+  const T* __restrict__ Bm = static_cast<const T*>(a.B) + (long)g * N;
+  const T* __restrict__ Cm = static_cast<const T*>(a.C) + (long)g * N;
+  const T* __restrict__ z = a.z ? static_cast<const T*>(a.z) + (long)h * P + p0 : nullptr;
+  T* __restrict__ y = static_cast<T*>(a.y) + (long)h * P + p0;
+  const float rate = -expf(a.A_log[h]);
+  const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const float skip = a.D ? a.D[h] : 0.f;
+
+  const long sbase = ((long)seq * a.H + h) * N * P + p0 + col;
+  float S[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) S[i] = a.S0 ? a.S0[sbase + (long)(ng * NR + i) * P] : 0.f;
+
+  for (int t0 = 0; t0 < sp.len; t0 += kTile) {
+    const int nt = min(kTile, sp.len - t0);
+    __syncthreads();
+    for (int i = tid; i < nt * N; i += kSimtThreads) {
+      const int t = i / N, n = i % N;
+      const long r = sp.row0 + t0 + t;
+      sB[t][n] = to_f(Bm[r * a.ldb + n]);
+      sC[t][n] = to_f(Cm[r * a.ldc + n]);
+    }
+    for (int i = tid; i < nt * PT; i += kSimtThreads) {
+      const int t = i / PT, p = i % PT;
+      sx[t][p] = to_f(x[(sp.row0 + t0 + t) * a.ldx + p]);
+    }
+    if (tid < nt) {
+      const float step = softplus(to_f(dt[(sp.row0 + t0 + tid) * a.lddt]) + bias);
+      s_step[tid] = step;
+      s_fade[tid] = expf(step * rate);
+    }
+    __syncthreads();
+    for (int t = 0; t < nt; ++t) {
+      const float fade = s_fade[t], xd = sx[t][col] * s_step[t];
+      float acc = 0.f;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        S[i] = fmaf(fade, S[i], xd * sB[t][ng * NR + i]);
+        acc = fmaf(S[i], sC[t][ng * NR + i], acc);
+      }
+      part[t][ng][col] = acc;
+    }
+    __syncthreads();
+    for (int i = tid; i < nt * PT; i += kSimtThreads) {
+      const int t = i / PT, p = i % PT;
+      const long r = sp.row0 + t0 + t;
+      float o = skip * sx[t][p];
+#pragma unroll
+      for (int q = 0; q < NG; ++q) o += part[t][q][p];
+      if (z) o *= silu(to_f(z[r * a.ldz + p]));
+      y[r * ((long)a.H * P) + p] = from_f<T>(o);
+    }
+  }
+  if (a.S_T) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) a.S_T[sbase + (long)(ng * NR + i) * P] = S[i];
+  }
+}
+
+}  // namespace ssm
+}  // namespace gdn

@@ -567,6 +567,126 @@ GDN_API gdn_status gdn_layer_fwd_static(const void *q_raw, const void *k_raw, co
                          float scale, float l2_eps, float norm_eps,
                          gdn_dtype dtype, gdn_dtype y_dtype, gdn_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Selective state space block: the sibling of the delta layer in a hybrid stack.  Its per-head state
+ * S [N, P] (fp32; N rows as d_k, P columns as d_v) has a scalar decay per head and token and no erase
+ * term, and its B and C are shared by groups of H / G consecutive heads (head h reads group h / (H/G)):
+ *      D_t = softplus(dt_t + dt_bias)
+ *      S_t = exp(-D_t exp(A_log)) S_{t-1} + D_t B_t x_t^T        y_t = (S_t^T C_t + D x_t) SiLU(z_t)
+ * x, B and C come from one short causal convolution over the channels [x | B | C].
+ * Token tensors of these calls may be columns of a wider row (a projection's output): `ld*` is the
+ * distance between two tokens in values; inside a token the heads (groups) lie one after the other.
+ * Pointers of token tensors need their element's alignment only, states 16 bytes (y of the scan
+ * too), weights 4; 16-byte aligned tensors whose ld* are multiples of 8 take the fast kernels.
+ * P and N are 16, 32, 64 or 128 (else GDN_ERR_UNSUPPORTED).  Inputs are expected finite: in the
+ * tensor-core scan a NaN or infinity in one of a head's tokens may reach that head's outputs up to
+ * 127 tokens before it, never another sequence's.
+ * ---------------------------------------------------------------------------------------------- */
+
+/*
+ * Short causal convolution of 4 taps with bias, then SiLU:
+ *      out[t][c] = SiLU(bias[c] + sum_{j=0..3} w[c][j] x[t - 3 + j][c])
+ *   x [B, T, C] (rows ldx apart), out [B, T, C] (dtype); w [C, 4] float (tap 3 on the current
+ *        token), bias [C] float or NULL
+ *   hist_in [B, 3, C] (dtype) or NULL (zeros): the raw rows of the three tokens before, oldest first
+ *   hist_out [B, 3, C] (dtype) or NULL: the last three raw rows of [history; this call's rows], for
+ *        the next piece or gdn_ssm_step; must not overlap hist_in.  A sequence without rows hands
+ *        its history on.
+ */
+GDN_API gdn_status gdn_ssm_conv(const void *x, long long ldx, const float *w, const float *bias,
+                        const void *hist_in, void *out, void *hist_out, int B, int T, int C,
+                        gdn_dtype dtype, gdn_stream_t stream);
+
+/* gdn_ssm_conv over packed sequences: x, out [total_T, C]; cu_seqlens, max_seqlen as
+ * gdn_chunk_fwd_varlen; hist_in, hist_out [nseq, 3, C].  No sequence reads a neighbour's rows; rows
+ * in no sequence keep their out. */
+GDN_API gdn_status gdn_ssm_conv_varlen(const void *x, long long ldx, const float *w,
+                        const float *bias, const int *cu_seqlens, int nseq, int max_seqlen,
+                        const void *hist_in, void *out, void *hist_out, int total_T, int C,
+                        gdn_dtype dtype, gdn_stream_t stream);
+
+/*
+ * The selective scan over whole prompts.
+ *   x [B, T, H, P], dt [B, T, H], Bm, Cm [B, T, G, N], z [B, T, H, P] or NULL (no gate)   (dtype)
+ *   A_log [H] float; D, dt_bias [H] float or NULL (zeros)
+ *   S0 [B, H, N, P] float or NULL (zeros); y [B, T, H, P] (dtype, without gaps);
+ *   S_T [B, H, N, P] float or NULL: the state after the last token (may not be S0's memory)
+ *   workspace: gdn_ssm_scan_workspace_bytes(...) bytes, 256-byte aligned (NULL when that is 0)
+ * bf16 with P and N in {64, 128}, 16-byte aligned x, Bm, Cm and ldx, ldb, ldc multiples of 8, run on
+ * the tensor cores; everything else on the CUDA cores.  The state's updates are exact to fp32
+ * rounding in both: the tensor-core kernel feeds them as three bf16 terms.
+ */
+GDN_API gdn_status gdn_ssm_scan(const void *x, long long ldx, const void *dt, long long lddt,
+                        const void *Bm, long long ldb, const void *Cm, long long ldc, const void *z,
+                        long long ldz, const float *A_log, const float *D, const float *dt_bias,
+                        const float *S0, void *y, float *S_T, void *workspace,
+                        size_t workspace_bytes, int B, int T, int H, int G, int P, int N,
+                        gdn_dtype dtype, gdn_stream_t stream);
+
+/* gdn_ssm_scan over packed sequences: [total_T, ...] token tensors, S0, S_T [nseq, H, N, P];
+ * cu_seqlens, max_seqlen as gdn_chunk_fwd_varlen.  Rows in no sequence keep their y; an empty
+ * sequence hands its S0 on. */
+GDN_API gdn_status gdn_ssm_scan_varlen(const void *x, long long ldx, const void *dt,
+                        long long lddt, const void *Bm, long long ldb, const void *Cm, long long ldc,
+                        const void *z, long long ldz, const float *A_log, const float *D,
+                        const float *dt_bias, const int *cu_seqlens, int nseq, int max_seqlen,
+                        const float *S0, void *y, float *S_T, void *workspace,
+                        size_t workspace_bytes, int total_T, int H, int G, int P, int N,
+                        gdn_dtype dtype, gdn_stream_t stream);
+
+/* Device scratch bytes of both scans for nseq sequences of at most max_seqlen tokens (host only,
+ * no CUDA call; 0 for sizes that the calls reject). */
+GDN_API size_t gdn_ssm_scan_workspace_bytes(int nseq, int max_seqlen, int H, int G, int P, int N,
+                        gdn_dtype dtype);
+
+/*
+ * One token of the block for n sequences in one kernel: the convolution over the carried history,
+ * the state update in place and the gated read-out.  It equals gdn_ssm_conv and gdn_ssm_scan one
+ * token at a time, except that x, B and C stay in fp32 between them.
+ *   u [n, H P + 2 G N]: raw rows [x | B | C]; dt [n, H]; z [n, H, P] or NULL            (dtype)
+ *   hist_in, hist_out [n, 3, H P + 2 G N] (dtype): must not overlap (swap them between steps)
+ *   w [H P + 2 G N, 4], bias [H P + 2 G N] or NULL, A_log, D, dt_bias as above
+ *   S [n, H, N, P] float, in place; y [n, H, P] (dtype)
+ */
+GDN_API gdn_status gdn_ssm_step(const void *u, long long ldu, const void *dt, long long lddt,
+                        const void *z, long long ldz, const void *hist_in, void *hist_out,
+                        const float *w, const float *bias, const float *A_log, const float *D,
+                        const float *dt_bias, float *S, void *y, int n, int H, int G, int P, int N,
+                        gdn_dtype dtype, gdn_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * The norms before and after a block, fused with its gate and its residual scale.
+ *      n = RMSNorm(y) w_post      h_out = h + res_scale SiLU(z) n      x = RMSNorm(h_out) w_pre
+ * ("Les briques d'un réseau de neurones", 2. SiLU and 4. RMSNorm.)
+ *   y, z, x [rows, D] (dtype); h, h_out [rows, D] (h_dtype: dtype, or GDN_F32 for bf16 dtype)
+ *   w_post, w_pre, res_scale [D] float.  Each may be NULL: without w_post n = y, without res_scale it
+ *        is 1, without z there is no gate, without w_pre x is not computed (x must be NULL too).
+ * Any D; element alignment is enough.  D a multiple of 8 up to 8192 with 16-byte aligned tensors
+ * takes the streaming kernels.  Outputs must not overlap inputs.
+ * ---------------------------------------------------------------------------------------------- */
+GDN_API gdn_status gdn_block_norm(const void *y, const void *h, const void *z, const float *w_post,
+                        const float *w_pre, const float *res_scale, void *h_out, void *x,
+                        long long rows, int D, float eps, gdn_dtype dtype, gdn_dtype h_dtype,
+                        gdn_stream_t stream);
+
+/*
+ * Its backward: gradients of <dh_out, h_out> + <dx, x>, from y, h_out (not h) and z.
+ *   dh_out [rows, D] (h_dtype), may be NULL with w_pre (zeros); dx [rows, D] (dtype), with w_pre
+ *   dy, dz [rows, D] (dtype; dz with z); dh [rows, D] (h_dtype)
+ *   dw_post, dw_pre, dres_scale [D] float, each present exactly when its vector is; sums over the
+ *        rows in a fixed order (reproducible bit for bit), zeros for rows = 0
+ *   workspace: gdn_block_norm_bwd_workspace_bytes(rows, D) bytes, 256-byte aligned
+ */
+GDN_API gdn_status gdn_block_norm_bwd(const void *y, const void *h_out, const void *z,
+                        const void *dh_out, const void *dx, const float *w_post,
+                        const float *w_pre, const float *res_scale, void *dy, void *dh, void *dz,
+                        float *dw_post, float *dw_pre, float *dres_scale, void *workspace,
+                        size_t workspace_bytes, long long rows, int D, float eps, gdn_dtype dtype,
+                        gdn_dtype h_dtype, gdn_stream_t stream);
+
+/* Device scratch bytes gdn_block_norm_bwd needs (host only, no CUDA call). */
+GDN_API size_t gdn_block_norm_bwd_workspace_bytes(long long rows, int D);
+
 #ifdef __cplusplus
 }
 #endif
