@@ -5,6 +5,7 @@
 #include "gdn.h"
 #include "ssm_conv.cuh"
 #include "ssm_scan_simt.cuh"
+#include "ssm_scan_tc.cuh"
 #include "ssm_step.cuh"
 
 using namespace gdn;
@@ -96,8 +97,8 @@ gdn_status check_heads(int H, int G, int P, int N) {
 }
 
 size_t scan_workspace(int nseq, int max_len, int H, int G, int P, int N, gdn_dtype dtype) {
-  (void)nseq, (void)max_len, (void)H, (void)G, (void)P, (void)N, (void)dtype;
-  return 0;
+  if (dtype != GDN_BF16 || !ssm::tcs::supported(P, N)) return 0;
+  return ssm::tcs::workspace(nseq, max_len, H, G, P, N);
 }
 
 gdn_status scan_call(ssm::ScanArgs a, int P, int N, void* workspace, size_t workspace_bytes, gdn_dtype dtype,
@@ -125,6 +126,16 @@ gdn_status scan_call(ssm::ScanArgs a, int P, int N, void* workspace, size_t work
   if (need && rows > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return GDN_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const void* tiles[] = {a.x, a.B, a.C};
+  bool tc = dtype == GDN_BF16 && ssm::tcs::supported(P, N) && rows > 0 && rows <= 0x7fffffffL - 2 * ssm::tcs::L &&
+            a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0;
+  for (const void* p : tiles) tc = tc && aligned(p, 16);
+  if (tc) {
+    if (P == 64) return (gdn_status)(N == 64 ? ssm::tcs::launch_np<64, 64>(a, workspace, st)
+                                             : ssm::tcs::launch_np<128, 64>(a, workspace, st));
+    return (gdn_status)(N == 64 ? ssm::tcs::launch_np<64, 128>(a, workspace, st)
+                                : ssm::tcs::launch_np<128, 128>(a, workspace, st));
+  }
   return dtype == GDN_F32 ? simt_scan<float>(N, P, a, st) : simt_scan<bf>(N, P, a, st);
 }
 
