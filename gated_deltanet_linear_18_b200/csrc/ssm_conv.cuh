@@ -10,7 +10,7 @@
 // three rows are read twice (3 / R more reads, from L2).
 #pragma once
 
-#include "common.cuh"
+#include "ssm_common.cuh"
 
 namespace gdn {
 namespace ssm {
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a) {
             acc = fmaf(w[1][e], w1[e], acc);
             acc = fmaf(w[2][e], w2[e], acc);
             acc = fmaf(w[3][e], u[e], acc);
-            o[e] = __fdividef(acc, 1.0f + __expf(-acc));
+            o[e] = silu(acc);
           }
           Pc::store(out + r * C, o);
         }

@@ -21,8 +21,13 @@
 // that matter, keep their relative accuracy.  Across blocks P's factor is a product of a row's and a
 // column's exponential (both at most 1), so only the diagonal 32 x 32 blocks need one exponential each.
 //
-// Roles (10 warps): warps 0-7 form operands and epilogues, warp 8 moves tiles (TMA), warp 9 issues the
-// MMAs.  x tiles are loaded a chunk ahead; y goes back through the x tile's memory by a TMA store.
+// Roles: four warpgroups that run ahead of one another as far as the tiles and accumulators allow.
+//   warp 0 loads B and C, warp 2 loads x tiles and stores y, warp 1 issues the MMAs in the order
+//     U (first 64 tokens), G, U (last 64), Yi, Ya of each chunk;
+//   warpgroup 1 forms the decays and X' of the next chunk while this one is multiplied (it reads x from
+//     global memory into registers, so that the x tile can hold y until that is stored);
+//   warpgroup 2 forms P and keeps the state in registers (a thread a row hp of S^T);
+//   warpgroup 3 forms y, in place of x in its tile, which leaves by a TMA store.
 // B and C, which the heads of a group share, come from L2.
 //
 // A sequence may be cut into segments that run side by side: a first launch (kOut = false) leaves
@@ -41,8 +46,7 @@ namespace ssm {
 namespace tcs {
 
 constexpr int L = 128;                        // tokens of a chunk
-constexpr int kWorkers = 256;                 // threads of the eight worker warps
-constexpr int kThreads = kWorkers + 64;
+constexpr int kThreads = 512;
 constexpr uint64_t kBudget = 4000000000ull;   // wait budget in SM cycles (about 2 s)
 constexpr uint32_t kTile = L * 128;           // bytes of a [128 rows, 64 bf16] tile
 using bf16_t = __nv_bfloat16;
@@ -55,27 +59,48 @@ struct Args {
   int z_vec;                    // z's rows allow 16-byte loads
 };
 
-// Vectors of a chunk (two, by the chunk's parity): u, w, e [2 heads][128]; (prefix, step) [2][128] pairs;
+// Vectors of a chunk (a ring of three): u, w, e, prefix, prefix - log2 step [2 heads][128];
 // block sums [2][4]; decay [2].
 constexpr uint32_t kVec = (2 * 128 * 5 + 16) * 4;
 
-// Shared memory: x tiles (two chunks), B, C, the state operand, X' staging, vectors, barriers.
+// Shared memory.  With the outputs: x tiles of two chunks, B, C, the state operand, X' of 64 tokens, vectors,
+// barriers.  Without: B of two chunks, X' of 128 tokens.
 template <int N, bool kOut> struct Layout {
   static constexpr uint32_t NB = N / 64;
   static constexpr uint32_t x = 0;                                  // [2][2] tiles
-  static constexpr uint32_t b = 4 * kTile;
-  static constexpr uint32_t c = b + NB * kTile;                     // kOut only
+  static constexpr uint32_t b = kOut ? 4 * kTile : 0;               // [1 or 2][NB] tiles
+  static constexpr uint32_t c = b + (kOut ? 1 : 2) * NB * kTile;
   static constexpr uint32_t s = c + (kOut ? NB * kTile : 0);
-  static constexpr uint32_t xw = s + (kOut ? NB * kTile : 0);       // [stages][3 terms][2] half tiles
+  static constexpr uint32_t xw = s + (kOut ? NB * kTile : 0);       // [1 or 2][3 terms][2] half tiles
   static constexpr uint32_t xw_stage = 6 * kTile / 2;
   static constexpr uint32_t vec = xw + (kOut ? 1 : 2) * xw_stage;
-  static constexpr uint32_t bars = vec + 2 * kVec;
+  static constexpr uint32_t bars = vec + 3 * kVec;
   static constexpr uint32_t bytes = bars + 256;
   static constexpr uint32_t alloc = bytes + 1024;                   // the base is rounded up to 1024
   static_assert(alloc <= 232448, "shared memory of a CTA");
 };
 
-enum Bar { XF = 0, BF = 2, CF, GD, CFREE, U0, YA, U1, XT, PR, SR, YR, DRAIN, kBars };
+// Barriers.  By TMA: XF (two x tiles), BF (two B buffers), CF.  By MMA commits: U0, U1 (U's halves), BE (two B buffers
+// free again), GD (G), YI, YA.  By the 128 threads of a warpgroup: XT0, XT1 (X' halves and the chunk's vectors), PR
+// (P), UR (U is in registers), SR (the state operand), YR (y in its tile, Yi and Ya read).
+// A wait names a phase by its parity alone, so each one below stands where the phase after the awaited
+// one cannot have completed: what completes that needs something this waiter has yet to do.  For the same
+// reason nobody but the MMA thread waits for XT0 / XT1; G, U and Y being complete implies the vectors.
+// log2 of a time step (0 gives -infinity: that token's weight is 0)
+__device__ __forceinline__ float log2_step(float v) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+enum Bar { XF = 0, BF = 2, CF = 4, U0, U1, BE, GD = BE + 2, YI, YA, XT0, XT1, PR, UR, SR, YR, DRAIN, kBars };
+
+template <int kRegs> __device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs> __device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1) {
   asm volatile(
@@ -108,6 +133,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 template <int N, int P, bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
@@ -115,8 +152,8 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   using Lay = Layout<N, kOut>;
   constexpr int NH = 128 / P;                 // heads of this CTA
   constexpr int NB = N / 64;
-  constexpr int NR = N / 2;                   // state columns of a worker thread
-  constexpr uint32_t TG = 0, TYI = 128, TYA = 256, TU = 384;
+  constexpr uint32_t TG = 0, TYI = 128, TYA = 256, TU = kOut ? 384 : 0;
+  constexpr uint32_t kTmem = kOut ? 512 : 128;
   const ScanArgs& a = k.a;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -141,15 +178,12 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::bars + kBars * 8 + 8);
   auto bar = [&](int i) { return sb + Lay::bars + 8u * i; };
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) {
-      const bool workers = i == XT || i == PR || i == SR || i == YR;
-      tc::mbar_init(tc::smem_u32(&bars[i]), workers ? kWorkers : 1);
-    }
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(tc::smem_u32(&bars[i]), i >= XT0 && i <= YR ? 128 : 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
-  if (warp == 9) tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
-  if (NH == 2 && heads == 1) {                // the missing head's x tiles: zeros, never loaded
+  if (warp == 1) tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmem);
+  if (kOut && NH == 2 && heads == 1) {        // the missing head's x tiles: zeros, never loaded
     for (int i = tid; i < 2 * (int)kTile / 16; i += kThreads) {
       const int buf = i / ((int)kTile / 16), o = i % ((int)kTile / 16);
       tc::st_shared_v4(sb + Lay::x + (2 * buf + 1) * kTile + o * 16, 0, 0, 0, 0);
@@ -161,297 +195,366 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto wait = [&](int b, int phase) { tc::mbar_wait(bar(b), (uint32_t)phase & 1u, abort_flag, kBudget); };
+  const int row0 = (int)(sp.row0 + (long)ch0 * L);        // this segment's first row
+  const int wg = warp >> 2, q = warp & 3;                 // warpgroup; lane quadrant
+  const int t = tid & 127;                                // a token's (or hp's) row
+  const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
+  auto vec_of = [&](int c) { return reinterpret_cast<float*>(smem + Lay::vec + (c % 3) * kVec); };
+  // a chunk's vectors: u [2][128] D_s exp(suffix in its block), w [2][128] D_s exp(suffix in the chunk), e [2][128]
+  // exp(prefix in the chunk), prefix in its block [2][128], the same less log2 D_s [2][128], block sums [2][4], exp(chunk's sum) [2]
+  constexpr int VU = 0, VW = 256, VE = 512, VP = 768, VT = 1280, VD = 1288;
 
-  if (warp == 8) {
-    // ----------------------------------- tiles -----------------------------------------------
+  if (wg == 0) {
+    regs_dec<80>();          // 80 + 96 + 208 + 128: the 512 registers of four threads at launch
     if (lane == 0 && nc > 0) {
-      const int row = (int)(sp.row0 + (long)ch0 * L);
-      auto load_x = [&](int c) {
-        const uint32_t dst = sb + Lay::x + (c & 1) * 2 * kTile;
-        tc::mbar_arrive_expect_tx(bar(XF + (c & 1)), (NH == 2 && heads == 1 ? 1 : 2) * kTile);
-        tma_load_2d(dst, &mx, bar(XF + (c & 1)), h0 * P, row + c * L);
-        if (NH == 1 || heads == 2) tma_load_2d(dst + kTile, &mx, bar(XF + (c & 1)), h0 * P + 64, row + c * L);
-      };
-      auto load_n = [&](uint32_t dst, const CUtensorMap* m, int b, int c) {
-        tc::mbar_arrive_expect_tx(bar(b), NB * kTile);
-        for (int i = 0; i < NB; ++i) tma_load_2d(dst + i * kTile, m, bar(b), g * N + i * 64, row + c * L);
-      };
-      int xs = 0, bs = 0, cs = 0;             // loads issued
-      load_x(xs++);
-      load_n(sb + Lay::b, &mb, BF, bs++);
-      if (kOut) load_n(sb + Lay::c, &mc, CF, cs++);
-      if (nc > 1) load_x(xs++);
-      for (int c = 0; c < nc && !*abort_flag; ++c) {
-        const bool more = c + 1 < nc;
-        if (kOut) {
-          if (more) {
-            wait(CFREE, c);
+      volatile int never = 0;
+      if (warp == 0) {
+        // --------------------------------- B and C ---------------------------------------------
+        auto load_n = [&](uint32_t dst, const CUtensorMap* m, int b, int c) {
+          tc::mbar_arrive_expect_tx(bar(b), NB * kTile);
+          for (int i = 0; i < NB; ++i) tma_load_2d(dst + i * kTile, m, bar(b), g * N + i * 64, row0 + c * L);
+        };
+        int bs = 0, cs = 0;                   // loads issued
+        auto load_b = [&] {
+          const int buf = kOut ? 0 : bs & 1;
+          load_n(sb + Lay::b + buf * NB * kTile, &mb, BF + buf, bs);
+          ++bs;
+        };
+        load_b();
+        if (kOut) load_n(sb + Lay::c, &mc, CF, cs++);
+        else if (nc > 1) load_b();
+        for (int c = 0; c < nc && !*abort_flag; ++c) {
+          if (kOut) wait(U1, c);
+          else wait(BE + (c & 1), c >> 1);
+          if (bs < nc) load_b();
+          if (kOut && cs < nc) {
+            wait(YI, c);
             load_n(sb + Lay::c, &mc, CF, cs++);
           }
-          wait(YR, c);
-          if (sp.len - (ch0 + c) * L >= L) {
-            const uint32_t src = sb + Lay::x + (c & 1) * 2 * kTile;
-            tma_store_2d(&my, src, h0 * P, row + c * L);
-            if (NH == 1 || heads == 2) tma_store_2d(&my, src + kTile, h0 * P + 64, row + c * L);
-            tc::bulk_commit();
-          }
         }
-        wait(U1, c);
-        if (more) load_n(sb + Lay::b, &mb, BF, bs++);
-        if (c + 2 < nc) {
-          if (kOut) tc::bulk_wait_read_all();
-          load_x(xs++);
-        }
-      }
-      // every load issued lands, and every store has read its source, before the CTA can leave
-      volatile int never = 0;
-      if (kOut) tc::bulk_wait_all();
-      for (int i = max(0, xs - 2); i < xs; ++i) tc::mbar_wait(bar(XF + (i & 1)), (i >> 1) & 1, &never, kBudget / 4);
-      tc::mbar_wait(bar(BF), (bs - 1) & 1, &never, kBudget / 4);
-      if (kOut) tc::mbar_wait(bar(CF), (cs - 1) & 1, &never, kBudget / 4);
-    }
-  } else if (warp == 9) {
-    // ----------------------------------- MMAs ------------------------------------------------
-    if (lane == 0 && nc > 0) {
-      constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, false, false);
-      constexpr uint32_t ID_YA = tc::idesc_bf16(128, P, false, true);
-      constexpr uint32_t ID_U = tc::idesc_bf16(128, N, true, true);
-      const uint64_t dc = tc::sdesc_sw128(sb + Lay::c, 16, 1024);          // C, K = n
-      const uint64_t db = tc::sdesc_sw128(sb + Lay::b, 16, 1024);          // B, K = n
-      const uint64_t dbt = tc::sdesc_sw128(sb + Lay::b, kTile, 1024);      // B, K = t
-      const uint64_t ds = tc::sdesc_sw128(sb + Lay::s, 16, 1024);          // S^T, K = n
-      for (int c = 0; c < nc; ++c) {
-        const uint64_t dx = tc::sdesc_sw128(sb + Lay::x + (c & 1) * 2 * kTile, kTile, 1024);
-        wait(BF, c);
+        // every load issued lands before the CTA can leave
         if (kOut) {
-          wait(CF, c);
-          tc::tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < NB * 4; ++i) {
-            const uint32_t o = (i >> 2) * kTile + (i & 3) * 32;
-            tc::mma_bf16(tmem + TG, tc::desc_adv(dc, o), tc::desc_adv(db, o), ID_G, i > 0);
+          tc::mbar_wait(bar(BF), (bs - 1) & 1, &never, kBudget / 4);
+          tc::mbar_wait(bar(CF), (cs - 1) & 1, &never, kBudget / 4);
+        } else {
+          for (int i = max(0, bs - 2); i < bs; ++i) tc::mbar_wait(bar(BF + (i & 1)), (i >> 1) & 1, &never, kBudget / 4);
+        }
+      } else if (warp == 2) {
+        // --------------------------------- x and y ---------------------------------------------
+        if constexpr (kOut) {
+          int xs = 0;
+          auto load_x = [&] {
+            const uint32_t dst = sb + Lay::x + (xs & 1) * 2 * kTile, b = bar(XF + (xs & 1));
+            tc::mbar_arrive_expect_tx(b, (NH == 2 && heads == 1 ? 1 : 2) * kTile);
+            tma_load_2d(dst, &mx, b, h0 * P, row0 + xs * L);
+            if (NH == 1 || heads == 2) tma_load_2d(dst + kTile, &mx, b, h0 * P + 64, row0 + xs * L);
+            ++xs;
+          };
+          load_x();
+          if (nc > 1) load_x();
+          for (int c = 0; c < nc && !*abort_flag; ++c) {
+            wait(YR, c);
+            if (sp.len - (ch0 + c) * L >= L) {
+              const uint32_t src = sb + Lay::x + (c & 1) * 2 * kTile;
+              tma_store_2d(&my, src, h0 * P, row0 + c * L);
+              if (NH == 1 || heads == 2) tma_store_2d(&my, src + kTile, h0 * P + 64, row0 + c * L);
+              tc::bulk_commit();
+            }
+            if (xs < nc) {
+              tc::bulk_wait_read_all();
+              load_x();
+            }
           }
-          tc::mma_commit(bar(GD));
-          wait(SR, c);
-          tc::tc_fence_after();
+          tc::bulk_wait_all();                // every store has read its source before the CTA can leave
+          for (int i = max(0, xs - 2); i < xs; ++i) tc::mbar_wait(bar(XF + (i & 1)), (i >> 1) & 1, &never, kBudget / 4);
+        }
+      } else if (warp == 1) {
+        // ----------------------------------- MMAs ----------------------------------------------
+        constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, false, false);
+        constexpr uint32_t ID_YA = tc::idesc_bf16(128, P, false, true);
+        constexpr uint32_t ID_U = tc::idesc_bf16(128, N, true, true);
+        const uint64_t dc = tc::sdesc_sw128(sb + Lay::c, 16, 1024);          // C, K = n
+        const uint64_t db = tc::sdesc_sw128(sb + Lay::b, 16, 1024);          // B, K = n
+        const uint64_t ds = tc::sdesc_sw128(sb + Lay::s, 16, 1024);          // S^T, K = n
+        auto spin = [&](int b, int phase) { tc::mbar_wait_spin(bar(b), (uint32_t)phase & 1u, abort_flag, kBudget); };
+        for (int c = 0; c < nc; ++c) {
+          const int bbuf = kOut ? 0 : c & 1;
+          const uint64_t dbt = tc::sdesc_sw128(sb + Lay::b + bbuf * NB * kTile, kTile, 1024);   // B, K = t
+          // half `hf` of the chunk's tokens: 4 steps of 16 for each of the three terms
+          auto issue_u = [&](int hf) {
+            const uint64_t dw = tc::sdesc_sw128(sb + Lay::xw + (kOut ? 0 : hf) * Lay::xw_stage, kTile / 2, 1024);
+#pragma unroll 1
+            for (int term = 0; term < 3; ++term)
 #pragma unroll
-          for (int i = 0; i < NB * 4; ++i) {
-            const uint32_t o = (i >> 2) * kTile + (i & 3) * 32;
-            tc::mma_bf16(tmem + TYI, tc::desc_adv(dc, o), tc::desc_adv(ds, o), ID_G, i > 0);
+              for (int i = 0; i < 4; ++i)
+                tc::mma_bf16(tmem + TU, tc::desc_adv(dw, term * kTile + i * 2048),
+                             tc::desc_adv(dbt, hf * (kTile / 2) + i * 2048), ID_U, hf + term + i > 0);
+          };
+          spin(BF + bbuf, kOut ? c : c >> 1);
+          spin(XT0, c);
+          if (c > 0) spin(UR, c - 1);
+          tc::tc_fence_after();
+          issue_u(0);
+          tc::mma_commit(bar(U0));
+          if constexpr (kOut) {
+            spin(CF, c);
+            tc::tc_fence_after();
+#pragma unroll 4
+            for (int i = 0; i < NB * 4; ++i) {
+              const uint32_t o = (i >> 2) * kTile + (i & 3) * 32;
+              tc::mma_bf16(tmem + TG, tc::desc_adv(dc, o), tc::desc_adv(db, o), ID_G, i > 0);
+            }
+            tc::mma_commit(bar(GD));
           }
-          tc::mma_commit(bar(CFREE));
-        }
-        // half `hf` of the chunk's tokens: 4 steps of 16 for each of the three terms
-        auto issue_u = [&](int hf) {
-          const uint64_t dw =
-              tc::sdesc_sw128(sb + Lay::xw + (kOut ? 0 : hf) * Lay::xw_stage, kTile / 2, 1024);
-#pragma unroll
-          for (int i = 0; i < 12; ++i)
-            tc::mma_bf16(tmem + TU, tc::desc_adv(dw, (i >> 2) * kTile + (i & 3) * 2048),
-                         tc::desc_adv(dbt, hf * (kTile / 2) + (i & 3) * 2048), ID_U, hf > 0 || i > 0);
-        };
-        wait(XT, 0);
-        tc::tc_fence_after();
-        issue_u(0);
-        tc::mma_commit(bar(U0));
-        if (kOut) {
-          wait(PR, c);
+          spin(XT1, c);
           tc::tc_fence_after();
-#pragma unroll
-          for (int hs = 0; hs < NH; ++hs)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              mma_bf16_ta(tmem + TYA + hs * 64, tmem + TG + 32 * (i >> 1) + 16 * hs + 8 * (i & 1),
-                          tc::desc_adv(dx, hs * kTile + i * 2048), ID_YA, i > 0);
-          tc::mma_commit(bar(YA));
+          issue_u(1);
+          tc::mma_commit(bar(U1));
+          if constexpr (!kOut) tc::mma_commit(bar(BE + bbuf));
+          if constexpr (kOut) {
+            spin(SR, c);
+            if (c > 0) spin(YR, c - 1);
+            tc::tc_fence_after();
+#pragma unroll 4
+            for (int i = 0; i < NB * 4; ++i) {
+              const uint32_t o = (i >> 2) * kTile + (i & 3) * 32;
+              tc::mma_bf16(tmem + TYI, tc::desc_adv(dc, o), tc::desc_adv(ds, o), ID_G, i > 0);
+            }
+            tc::mma_commit(bar(YI));
+            spin(XF + (c & 1), c >> 1);
+            spin(PR, c);
+            tc::tc_fence_after();
+            const uint64_t dx = tc::sdesc_sw128(sb + Lay::x + (c & 1) * 2 * kTile, kTile, 1024);
+#pragma unroll 1
+            for (int hs = 0; hs < NH; ++hs)
+#pragma unroll 4
+              for (int i = 0; i < 8; ++i)
+                mma_bf16_ta(tmem + TYA + hs * 64, tmem + TG + 32 * (i >> 1) + 16 * hs + 8 * (i & 1),
+                            tc::desc_adv(dx, hs * kTile + i * 2048), ID_YA, i > 0);
+            tc::mma_commit(bar(YA));
+          }
         }
-        wait(XT, 1);
-        tc::tc_fence_after();
-        issue_u(1);
-        tc::mma_commit(bar(U1));
-      }
-      tc::mma_commit(bar(DRAIN));
-      volatile int never = 0;
-      tc::mbar_wait(bar(DRAIN), 0, &never, kBudget / 4);
-    }
-  } else {
-    // ----------------------------------- workers ---------------------------------------------
-    const int q = warp & 3, wg = warp >> 2;          // lane quadrant; half of the columns
-    const int t = tid & 127;                         // the row (of tokens, or of hp) of this thread
-    const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
-    const int vh = NH == 2 ? wg : 0;                 // the head whose vectors this thread forms
-    const bool vec_on = NH == 2 ? wg < heads : wg == 0;
-    const int sh = NH == 2 ? (t >> 6) : 0;           // the head of state row t
-    const int p = NH == 2 ? (t & 63) : t;
-    const bool s_on = sh < heads;
-    const int n0 = wg * NR;
-    float rate = 0.f, bias = 0.f;
-    if (vec_on) {
-      rate = -expf(a.A_log[h0 + vh]) * kLog2e;
-      bias = a.dt_bias ? a.dt_bias[h0 + vh] : 0.f;
-    }
-    const bool y_on = NH == 1 || wg < heads;
-    const float skip = kOut && a.D && y_on ? a.D[h0 + (NH == 2 ? wg : 0)] : 0.f;
-
-    // ---- the state before this segment
-    float S[NR];
-    const long HNP = (long)a.H * N * P;
-    const long srow = ((long)(h0 + sh) * N + n0) * P + p;    // state rows n0 .. n0 + NR - 1, column p
-    const float* wseg = k.ws + (long)seq * (k.segments - 1) * HNP + srow;
-    const float* wdec = k.ws + (long)a.nseq * (k.segments - 1) * HNP + (long)seq * (k.segments - 1) * a.H + h0 + sh;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) S[i] = 0.f;
-    if (s_on) {
-      if (seg == 0) {
-        if (a.S0) {
-#pragma unroll
-          for (int i = 0; i < NR; ++i) S[i] = a.S0[seq * HNP + srow + (long)i * P];
-        }
-      } else if (kOut) {
-        for (int j = 0; j < seg; ++j) {
-          const float d = wdec[(long)j * a.H];
-#pragma unroll
-          for (int i = 0; i < NR; ++i) S[i] = fmaf(d, S[i], wseg[j * HNP + (long)i * P]);
-        }
+        tc::mma_commit(bar(DRAIN));
+        tc::mbar_wait(bar(DRAIN), 0, &never, kBudget / 4);
       }
     }
-    float seg_decay = 1.f;
-    auto publish_state = [&]() {               // the copy that the next chunk's Yi reads
+  } else if (wg == 1 || (!kOut && wg == 3)) {
+    // ------------------------- the decays and X' (without outputs: a half each) ------------------
+    if (wg == 1) regs_dec<96>();
+    float rate[NH], bias[NH];
 #pragma unroll
-      for (int j = 0; j < NR / 8; ++j) {
-        const uint32_t chunk = N == 128 ? j : wg * 4 + j;
-        tc::st_shared_v4(sb + Lay::s + (N == 128 ? wg * kTile : 0) + tc::sw128(t, chunk),
-                         tc::pack_bf16(S[8 * j], S[8 * j + 1]), tc::pack_bf16(S[8 * j + 2], S[8 * j + 3]),
-                         tc::pack_bf16(S[8 * j + 4], S[8 * j + 5]), tc::pack_bf16(S[8 * j + 6], S[8 * j + 7]));
-      }
-      tc::fence_proxy_async_smem();
-      tc::tc_fence_before();
-      tc::mbar_arrive(bar(SR));
-    };
-    if (kOut && nc > 0) publish_state();
-
-    const bf16_t* dtp = static_cast<const bf16_t*>(a.dt) + h0 + vh;
-    auto load_dt = [&](int c) -> float {
+    for (int hs = 0; hs < NH; ++hs) {
+      rate[hs] = hs < heads ? -expf(a.A_log[h0 + hs]) * kLog2e : 0.f;
+      bias[hs] = hs < heads && a.dt_bias ? a.dt_bias[h0 + hs] : 0.f;
+    }
+    const bf16_t* dtp = static_cast<const bf16_t*>(a.dt) + h0;
+    const bf16_t* xp = static_cast<const bf16_t*>(a.x) + (long)h0 * P;
+    bf16_t raw[NH];                  // kept as loaded: a conversion would wait for the load at once
+    auto load_dt = [&](int c) {
       const int at = (ch0 + c) * L + t;
-      return vec_on && c < nc && at < sp.len ? __bfloat162float(dtp[(sp.row0 + at) * a.lddt]) : 0.f;
+#pragma unroll
+      for (int hs = 0; hs < NH; ++hs)
+        if (hs < heads && c < nc && at < sp.len) raw[hs] = dtp[(sp.row0 + at) * a.lddt + hs];
     };
-    float raw = load_dt(0);
+    // this thread's eight 16-byte pieces of a half: rows (t + 128 i) / 16, piece t % 16 of 16
+    const int j = t & 7, tile = (t >> 3) & 1, r0 = t >> 4;
+    uint4 xv[8];
+    auto load_x = [&](int c, int hf) {
+      const int at = (ch0 + c) * L + hf * 64 + r0;
+      const bf16_t* p = xp + (sp.row0 + at) * a.ldx + tile * 64 + j * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xv[i] = make_uint4(0, 0, 0, 0);
+        if (c < nc && at + 8 * i < sp.len && (NH == 1 || tile < heads))
+          xv[i] = *reinterpret_cast<const uint4*>(p + (long)(8 * i) * a.ldx);
+      }
+    };
+    load_dt(0);
+    load_x(0, kOut || wg == 1 ? 0 : 1);
     for (int c = 0; c < nc; ++c) {
+      float* vec = vec_of(c);
       const int valid = min(L, sp.len - (ch0 + c) * L);
-      const long row = sp.row0 + (long)(ch0 + c) * L;
-      float* vec = reinterpret_cast<float*>(smem + Lay::vec + (c & 1) * kVec);
-      float* u_ = vec;                          // [2][128] D_s exp(suffix in its block)
-      float* w_ = vec + 256;                    // [2][128] D_s exp(suffix in the chunk)
-      float* e_ = vec + 512;                    // [2][128] exp(prefix in the chunk)
-      float2* pd = reinterpret_cast<float2*>(vec + 768);   // [2][128] (prefix in its block, D_s)
-      float* tot = vec + 1280;                  // [2][4] block sums
-      float* dec = tot + 8;                     // [2] exp(sum of the chunk)
-      // ---- 1. the chunk's decays, in base-2 logarithms
-      if (NH == 2 || wg == 0) {
-        const bool live = vec_on && t < valid;
-        const float step = live ? softplus(raw + bias) : 0.f;
-        const float la = live ? step * rate : 0.f;
-        float pre = la, suf = la;
+      // ---- decays, in base-2 logarithms.  Their slot held chunk c - 3's: with outputs this thread has seen U0
+      // of chunk c - 1, issued after Yi of c - 2 and so after every reader of c - 3; without, U0 or U1 of c - 2.
+      float pre[NH], suf[NH], step[NH];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float up = __shfl_up_sync(0xffffffffu, pre, o);
-          const float dn = __shfl_down_sync(0xffffffffu, suf, o);
-          if (lane >= o) pre += up;
-          if (lane < 32 - o) suf += dn;
+      for (int hs = 0; hs < NH; ++hs) {
+        step[hs] = t < valid && hs < heads ? softplus(__bfloat162float(raw[hs]) + bias[hs]) : 0.f;
+        pre[hs] = suf[hs] = t < valid ? step[hs] * rate[hs] : 0.f;
+      }
+      load_dt(c + 1);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int hs = 0; hs < NH; ++hs) {
+          const float up = __shfl_up_sync(0xffffffffu, pre[hs], o);
+          const float dn = __shfl_down_sync(0xffffffffu, suf[hs], o);
+          if (lane >= o) pre[hs] += up;
+          if (lane < 32 - o) suf[hs] += dn;
         }
-        suf = __shfl_down_sync(0xffffffffu, suf, 1);         // the sum over the tokens after this one
+      }
+#pragma unroll
+      for (int hs = 0; hs < NH; ++hs) {
+        suf[hs] = __shfl_down_sync(0xffffffffu, suf[hs], 1);   // the sum over the tokens after this one
         if (lane == 31) {
-          suf = 0.f;
-          tot[vh * 4 + q] = pre;
+          suf[hs] = 0.f;
+          vec[VT + hs * 4 + q] = pre[hs];
         }
-        pd[vh * 128 + t] = make_float2(pre, step);
-        u_[vh * 128 + t] = step * tc::ex2(suf);
-        tc::named_bar(1 + vh, 128);
-        const float t0 = tot[vh * 4], t1 = tot[vh * 4 + 1], t2 = tot[vh * 4 + 2], t3 = tot[vh * 4 + 3];
-        const float before = q == 0 ? 0.f : q == 1 ? t0 : q == 2 ? t0 + t1 : t0 + t1 + t2;
-        const float after = q == 3 ? 0.f : q == 2 ? t3 : q == 1 ? t2 + t3 : t1 + t2 + t3;
-        w_[vh * 128 + t] = step * tc::ex2(suf + after);
-        e_[vh * 128 + t] = tc::ex2(pre + before);
-        if (t == 0) dec[vh] = tc::ex2(t0 + t1 + t2 + t3);
+        vec[VP + hs * 128 + t] = pre[hs];
+        vec[VP + 256 + hs * 128 + t] = pre[hs] - log2_step(step[hs]);
+        vec[VU + hs * 128 + t] = step[hs] * tc::ex2(suf[hs]);
       }
-      raw = load_dt(c + 1);
-      wait(XF + (c & 1), c >> 1);
-      const uint32_t xt = sb + Lay::x + (c & 1) * 2 * kTile;
-      if (valid < L) {       // rows behind the sequence reach no product: another sequence's, maybe NaN
-        wait(BF, c);
-        if (kOut) wait(GD, c);             // G reads the same B tile
-        for (int i = tid; i < (L - valid) * 8 * (2 + NB); i += kWorkers) {
-          const int j = i & 7, tile = (i >> 3) % (2 + NB), r = valid + (i >> 3) / (2 + NB);
-          tc::st_shared_v4((tile < 2 ? xt + tile * kTile : sb + Lay::b + (tile - 2) * kTile) + tc::sw128(r, j), 0, 0, 0, 0);
-        }
-      }
-      tc::named_bar(3, kWorkers);
-      // ---- 2. X' of half `hf` of the tokens, in three terms
-      auto weigh = [&](int hf) {
-        const uint32_t dst = sb + Lay::xw + (kOut ? 0 : hf) * Lay::xw_stage;
+      tc::named_bar(wg, 128);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int id = tid + kWorkers * i;
-          const int j = id & 7, r = (id >> 3) & 63, tile = id >> 9;
-          const uint4 v = tc::ld_shared_v4(xt + tile * kTile + tc::sw128(hf * 64 + r, j));
-          const float w = w_[(NH == 2 ? tile : 0) * 128 + hf * 64 + r];
-          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+      for (int hs = 0; hs < NH; ++hs) {
+        const float4 s4 = *reinterpret_cast<const float4*>(vec + VT + hs * 4);
+        const float before = q == 0 ? 0.f : q == 1 ? s4.x : q == 2 ? s4.x + s4.y : s4.x + s4.y + s4.z;
+        const float after = q == 3 ? 0.f : q == 2 ? s4.w : q == 1 ? s4.z + s4.w : s4.y + s4.z + s4.w;
+        vec[VW + hs * 128 + t] = step[hs] * tc::ex2(suf[hs] + after);
+        vec[VE + hs * 128 + t] = tc::ex2(pre[hs] + before);
+        if (t == 0) vec[VD + hs] = tc::ex2(s4.x + s4.y + s4.z + s4.w);
+      }
+      tc::named_bar(wg, 128);
+      if (kOut && valid < L) {   // rows behind the sequence reach no product: another sequence's, maybe NaN
+        // (G may be reading B meanwhile: it yields columns s >= valid, which no row t < valid keeps)
+        wait(XF + (c & 1), c >> 1);
+        wait(BF, c);
+        const uint32_t xt = sb + Lay::x + (c & 1) * 2 * kTile;
+        for (int i = t; i < (L - valid) * 8 * (2 + NB); i += 128) {
+          const int jj = i & 7, tl = (i >> 3) % (2 + NB), r = valid + (i >> 3) / (2 + NB);
+          tc::st_shared_v4((tl < 2 ? xt + tl * kTile : sb + Lay::b + (tl - 2) * kTile) + tc::sw128(r, jj), 0, 0, 0, 0);
+        }
+      }
+      // ---- X' of half `hf`: three bf16 terms that add up to the fp32 product.  (The loops of the roles are kept
+      // rolled where registers allow: four roles of unrolled code do not fit the instruction cache.)
+#pragma unroll 1
+      for (int hh = 0; hh < (kOut ? 2 : 1); ++hh) {
+        const int hf = kOut ? hh : (wg == 1 ? 0 : 1);
+        const uint32_t dst = sb + Lay::xw + (kOut ? 0 : hf) * Lay::xw_stage + tile * (kTile / 2);
+        // the staging is free again
+        if (kOut && hf) wait(U0, c);
+        else if (c > 0) wait(kOut || hf ? U1 : U0, c - 1);
+#pragma unroll 1
+        for (int i2 = 0; i2 < 4; ++i2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = r0 + 8 * (2 * i2 + i);
+          const float w = vec[VW + (NH == 2 ? tile : 0) * 128 + hf * 64 + r];
+          const uint64_t ww = tc::f2(w, w);
+          const uint32_t in[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
           uint32_t o0[4], o1[4], o2[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float f0 = tc::bf16lo(in[e]) * w, f1 = tc::bf16hi(in[e]) * w;
+            const uint64_t f = tc::mul2(tc::f2(tc::bf16lo(in[e]), tc::bf16hi(in[e])), ww);
+            float f0, f1;
+            tc::f2_get(f, f0, f1);
             o0[e] = tc::pack_bf16(f0, f1);
-            const float g0 = f0 - tc::bf16lo(o0[e]), g1 = f1 - tc::bf16hi(o0[e]);
-            o1[e] = tc::pack_bf16(g0, g1);
-            o2[e] = tc::pack_bf16(g0 - tc::bf16lo(o1[e]), g1 - tc::bf16hi(o1[e]));
+            const uint64_t g2 = tc::sub2(f, tc::f2(tc::bf16lo(o0[e]), tc::bf16hi(o0[e])));
+            tc::f2_get(g2, f0, f1);
+            o1[e] = tc::pack_bf16(f0, f1);
+            tc::f2_get(tc::sub2(g2, tc::f2(tc::bf16lo(o1[e]), tc::bf16hi(o1[e]))), f0, f1);
+            o2[e] = tc::pack_bf16(f0, f1);
           }
-          const uint32_t at = dst + tile * (kTile / 2) + tc::sw128(r, j);
+          const uint32_t at = dst + tc::sw128(r, j);
           tc::st_shared_v4(at, o0[0], o0[1], o0[2], o0[3]);
           tc::st_shared_v4(at + kTile, o1[0], o1[1], o1[2], o1[3]);
           tc::st_shared_v4(at + 2 * kTile, o2[0], o2[1], o2[2], o2[3]);
         }
+#pragma unroll
+        for (int i = 0; i < 6; ++i) xv[i] = xv[i + 2];
+        }
         tc::fence_proxy_async_smem();
-        tc::mbar_arrive(bar(XT));
-      };
-      weigh(0);
+        tc::mbar_arrive(bar(hf ? XT1 : XT0));
+        if (kOut) load_x(c + hh, hh ^ 1);            // the next half: of this chunk, then of the next
+        else load_x(c + 1, hf);
+      }
+    }
+  } else if (wg == 2) {
+    // ----------------------------------- P and the state -----------------------------------------
+    regs_inc<208>();
+    const int sh = NH == 2 ? (t >> 6) : 0;           // the head of state row t
+    const int p = NH == 2 ? (t & 63) : t;
+    const bool s_on = sh < heads;
+    float S[N];                                      // row (sh, p) of S^T
+    const long HNP = (long)a.H * N * P;
+    const long srow = (long)(h0 + sh) * N * P + p;
+    float* wseg = k.ws + (long)seq * (k.segments - 1) * HNP + srow;
+    float* wdec = k.ws + (long)a.nseq * (k.segments - 1) * HNP + (long)seq * (k.segments - 1) * a.H + h0 + sh;
+    // the state before: S0, or those of the segments before, in order; 32 columns at a time
+    const float* from0 = seg == 0 ? (a.S0 ? a.S0 + seq * HNP + srow : nullptr) : wseg;
+    const int sources = !s_on || !from0 ? 0 : seg == 0 ? 1 : kOut ? seg : 0;
+#pragma unroll
+    for (int i0 = 0; i0 < N; i0 += 32) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) S[i0 + i] = 0.f;
+#pragma unroll 1
+      for (int s = 0; s < sources; ++s) {
+        const float d = s > 0 ? wdec[(long)s * a.H] : 0.f;
+        const float* from = from0 + s * HNP + (long)i0 * P;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(d, S[i0 + i], from[(long)i * P]);
+      }
+    }
+    float seg_decay = 1.f;
+    auto publish_state = [&] {                       // the copy that the next chunk's Yi reads
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i)
+        tc::st_shared_v4(sb + Lay::s + (i >> 3) * kTile + tc::sw128(t, i & 7), tc::pack_bf16(S[8 * i], S[8 * i + 1]),
+                         tc::pack_bf16(S[8 * i + 2], S[8 * i + 3]), tc::pack_bf16(S[8 * i + 4], S[8 * i + 5]),
+                         tc::pack_bf16(S[8 * i + 6], S[8 * i + 7]));
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive(bar(SR));
+    };
+    if (kOut && nc > 0) publish_state();
+    for (int c = 0; c < nc; ++c) {
+      const float* vec = vec_of(c);
       if constexpr (kOut) {
-        // ---- 3. P from G, block of 32 columns by block
+        // ---- P from G, block of 32 columns by block
         wait(GD, c);
         tc::tc_fence_after();
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          if (b > q) {                               // after every token of these rows
+            uint32_t o[16];
 #pragma unroll
-        for (int bi = 0; bi < 2; ++bi) {
-          const int b = 2 * wg + bi;
-          float G[32];
-          if (b <= q) {
-            tc::tmem_ld32(tlane + TG + 32 * b, G);
-            tc::tmem_wait_ld();
+            for (int i = 0; i < 16; ++i) o[i] = 0;
+#pragma unroll
+            for (int hs = 0; hs < NH; ++hs) tmem_st16(tlane + TG + 32 * b + 16 * hs, o);
+            continue;
           }
-#pragma unroll
+          float G[32];
+          tc::tmem_ld32(tlane + TG + 32 * b, G);
+          tc::tmem_wait_ld();
+#pragma unroll 1
           for (int hs = 0; hs < NH; ++hs) {
             uint32_t o[16];
-            if (b > q) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = 0;
-            } else if (b < q) {
-              float mid = pd[hs * 128 + t].x;
-              for (int i = b + 1; i < q; ++i) mid += tot[hs * 4 + i];
+            const float mine = vec[VP + hs * 128 + t];
+            if (b < q) {
+              float mid = mine;
+              for (int i = b + 1; i < q; ++i) mid += vec[VT + hs * 4 + i];
               const float r = tc::ex2(mid);
-              const float4* u4 = reinterpret_cast<const float4*>(u_ + hs * 128 + 32 * b);
+              const uint64_t rr = tc::f2(r, r);
+              const float4* u4 = reinterpret_cast<const float4*>(vec + VU + hs * 128 + 32 * b);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float4 uu = u4[i];
-                o[2 * i] = tc::pack_bf16(G[4 * i] * (uu.x * r), G[4 * i + 1] * (uu.y * r));
-                o[2 * i + 1] = tc::pack_bf16(G[4 * i + 2] * (uu.z * r), G[4 * i + 3] * (uu.w * r));
+                const float4 u = u4[i];
+                float f0, f1;
+                tc::f2_get(tc::mul2(tc::f2(G[4 * i], G[4 * i + 1]), tc::mul2(tc::f2(u.x, u.y), rr)), f0, f1);
+                o[2 * i] = tc::pack_bf16(f0, f1);
+                tc::f2_get(tc::mul2(tc::f2(G[4 * i + 2], G[4 * i + 3]), tc::mul2(tc::f2(u.z, u.w), rr)), f0, f1);
+                o[2 * i + 1] = tc::pack_bf16(f0, f1);
               }
             } else {
-              const float mine = pd[hs * 128 + t].x;
-              const float4* p4 = reinterpret_cast<const float4*>(pd + hs * 128 + 32 * b);
+              const float4* p4 = reinterpret_cast<const float4*>(vec + VP + 256 + hs * 128 + 32 * b);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float4 v = p4[i];                 // (prefix, step) of columns 2 i and 2 i + 1
-                const float f0 = 2 * i <= lane ? G[2 * i] * (v.y * tc::ex2(mine - v.x)) : 0.f;
-                const float f1 = 2 * i + 1 <= lane ? G[2 * i + 1] * (v.w * tc::ex2(mine - v.z)) : 0.f;
-                o[i] = tc::pack_bf16(f0, f1);
+              for (int i = 0; i < 8; ++i) {
+                const float4 v = p4[i];              // prefix - log2 D of columns 4 i .. 4 i + 3
+                const float f0 = 4 * i <= lane ? G[4 * i] * tc::ex2(mine - v.x) : 0.f;
+                const float f1 = 4 * i + 1 <= lane ? G[4 * i + 1] * tc::ex2(mine - v.y) : 0.f;
+                const float f2 = 4 * i + 2 <= lane ? G[4 * i + 2] * tc::ex2(mine - v.z) : 0.f;
+                const float f3 = 4 * i + 3 <= lane ? G[4 * i + 3] * tc::ex2(mine - v.w) : 0.f;
+                o[2 * i] = tc::pack_bf16(f0, f1);
+                o[2 * i + 1] = tc::pack_bf16(f2, f3);
               }
             }
             tmem_st16(tlane + TG + 32 * b + 16 * hs, o);
@@ -461,88 +564,27 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         tc::tc_fence_before();
         tc::mbar_arrive(bar(PR));
       }
-      uint4 zr[8];
-      if constexpr (kOut) {
-        // the gate's values, needed in step 5
-        if (a.z && y_on && t < valid) {
-          const bf16_t* zp = static_cast<const bf16_t*>(a.z) + (row + t) * a.ldz + (long)h0 * P + wg * 64;
-          if (k.z_vec) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) zr[j] = reinterpret_cast<const uint4*>(zp)[j];
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = (uint32_t)__bfloat16_as_ushort(zp[8 * j + 2 * e]) |
-                       ((uint32_t)__bfloat16_as_ushort(zp[8 * j + 2 * e + 1]) << 16);
-              zr[j] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-          }
-        }
-        wait(U0, c);                       // the staging of the first half is free again
-      }
-      // ---- 4. the second half
-      weigh(1);
-      if constexpr (kOut) {
-        // ---- 5. y, in place of x
-        wait(YA, c);
-        tc::tc_fence_after();
-        tc::named_bar(3, kWorkers);        // every thread has read the x tile in step 4
-        const float e = e_[(NH == 2 ? wg : 0) * 128 + t];
-        bf16_t* yp = static_cast<bf16_t*>(a.y) + (row + t) * ((long)a.H * P) + (long)h0 * P + wg * 64;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float yi[32], ya[32];
-          tc::tmem_ld32(tlane + TYI + 64 * wg + 32 * hf, yi);
-          tc::tmem_ld32(tlane + TYA + 64 * wg + 32 * hf, ya);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t at = xt + wg * kTile + tc::sw128(t, 4 * hf + j);
-            const uint4 xv = tc::ld_shared_v4(at);
-            const uint32_t xi[4] = {xv.x, xv.y, xv.z, xv.w};
-            const uint4 z4 = zr[4 * hf + j];
-            const uint32_t zi[4] = {z4.x, z4.y, z4.z, z4.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int cidx = 8 * j + 2 * i;
-              float f0 = fmaf(e, yi[cidx], fmaf(skip, tc::bf16lo(xi[i]), ya[cidx]));
-              float f1 = fmaf(e, yi[cidx + 1], fmaf(skip, tc::bf16hi(xi[i]), ya[cidx + 1]));
-              if (a.z) {
-                f0 *= silu(tc::bf16lo(zi[i]));
-                f1 *= silu(tc::bf16hi(zi[i]));
-              }
-              o[i] = tc::pack_bf16(f0, f1);
-            }
-            if (!y_on) continue;
-            if (valid == L) tc::st_shared_v4(at, o[0], o[1], o[2], o[3]);
-            else if (t < valid)
-              *reinterpret_cast<uint4*>(yp + 32 * hf + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        }
-        tc::fence_proxy_async_smem();
-        tc::mbar_arrive(bar(YR));
-      }
-      // ---- 6. the state
+      // ---- S' = exp(c_L) S + U
       wait(U1, c);
       tc::tc_fence_after();
-      const float d = dec[sh];
+      const float d = vec[VD + sh];
       seg_decay *= d;
+      const uint64_t dd = tc::f2(d, d);
 #pragma unroll
-      for (int i = 0; i < NR / 32; ++i) {
+      for (int i = 0; i < N / 32; ++i) {
         float U[32];
-        tc::tmem_ld32(tlane + TU + n0 + 32 * i, U);
+        tc::tmem_ld32(tlane + TU + 32 * i, U);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[32 * i + j] = fmaf(d, S[32 * i + j], U[j]);
+        for (int e = 0; e < 32; e += 2)
+          tc::f2_get(tc::fma2(dd, tc::f2(S[32 * i + e], S[32 * i + e + 1]), tc::f2(U[e], U[e + 1])), S[32 * i + e],
+                     S[32 * i + e + 1]);
       }
-      if (kOut) {
-        if (c + 1 < nc) publish_state();
-      } else {
-        tc::tc_fence_before();             // U has been read before this thread's next X' lets U0 run again
+      tc::tc_fence_before();
+      tc::mbar_arrive(bar(UR));
+      if (kOut && c + 1 < nc) {
+        wait(YI, c);                                 // Yi has read the copy before
+        publish_state();
       }
     }
     // ---- the state after this segment
@@ -550,22 +592,106 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       if constexpr (kOut) {
         if (last && a.S_T) {
 #pragma unroll
-          for (int i = 0; i < NR; ++i) a.S_T[seq * HNP + srow + (long)i * P] = S[i];
+          for (int i = 0; i < N; ++i) a.S_T[seq * HNP + srow + (long)i * P] = S[i];
         }
       } else {
-        float* out = const_cast<float*>(wseg) + seg * HNP;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) out[(long)i * P] = S[i];
-        if (p == 0 && wg == 0) const_cast<float*>(wdec)[(long)seg * a.H] = seg_decay;
+        for (int i = 0; i < N; ++i) wseg[seg * HNP + (long)i * P] = S[i];
+        if (p == 0) wdec[(long)seg * a.H] = seg_decay;
+      }
+    }
+  } else {
+    // ------------------------------------------- y -----------------------------------------------
+    if constexpr (kOut) {
+      float skip[NH];
+#pragma unroll
+      for (int hs = 0; hs < NH; ++hs) skip[hs] = a.D && hs < heads ? a.D[h0 + hs] : 0.f;
+      const bool gated = a.z != nullptr;
+      for (int c = 0; c < nc; ++c) {
+        const int valid = min(L, sp.len - (ch0 + c) * L);
+        const long row = (long)row0 + c * L + t;
+        const uint32_t xt = sb + Lay::x + (c & 1) * 2 * kTile;
+        const bf16_t* zp = gated ? static_cast<const bf16_t*>(a.z) + row * a.ldz + (long)h0 * P : nullptr;
+        bf16_t* yp = static_cast<bf16_t*>(a.y) + row * ((long)a.H * P) + (long)h0 * P;
+        // the gate's values of 16 columns (piece i of eight)
+        auto load_z = [&](int i, uint4 (&zr)[2]) {
+          const bool on = gated && t < valid && (NH == 1 || (i >> 2) < heads);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            zr[e] = make_uint4(0, 0, 0, 0);
+            if (!on) continue;
+            const bf16_t* zq = zp + 16 * i + 8 * e;
+            if (k.z_vec) {
+              zr[e] = *reinterpret_cast<const uint4*>(zq);
+            } else {
+              uint32_t v[4];
+#pragma unroll
+              for (int f = 0; f < 4; ++f)
+                v[f] = (uint32_t)__bfloat16_as_ushort(zq[2 * f]) | ((uint32_t)__bfloat16_as_ushort(zq[2 * f + 1]) << 16);
+              zr[e] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        };
+        uint4 zr[2];
+        load_z(0, zr);
+        wait(XF + (c & 1), c >> 1);
+        wait(YA, c);
+        tc::tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const int hs = NH == 2 ? i >> 2 : 0;
+          const float dskip = NH == 2 && hs ? skip[NH - 1] : skip[0];
+          if (NH == 2 && hs >= heads) break;
+          const float e = vec_of(c)[VE + hs * 128 + t];
+          float yi[16], ya[16];
+          tmem_ld16(tlane + TYI + 16 * i, yi);
+          tmem_ld16(tlane + TYA + 16 * i, ya);
+          const uint32_t at0 = xt + (i >> 2) * kTile + tc::sw128(t, 2 * (i & 3));
+          const uint32_t at1 = xt + (i >> 2) * kTile + tc::sw128(t, 2 * (i & 3) + 1);
+          const uint4 xq[2] = {tc::ld_shared_v4(at0), tc::ld_shared_v4(at1)};
+          uint4 zn[2];
+          if (i < 7) load_z(i + 1, zn);
+          tc::tmem_wait_ld();
+          uint32_t o[2][4];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t xi[4] = {xq[m].x, xq[m].y, xq[m].z, xq[m].w};
+            const uint32_t zi[4] = {zr[m].x, zr[m].y, zr[m].z, zr[m].w};
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const int col = 8 * m + 2 * f;
+              float f0 = fmaf(e, yi[col], fmaf(dskip, tc::bf16lo(xi[f]), ya[col]));
+              float f1 = fmaf(e, yi[col + 1], fmaf(dskip, tc::bf16hi(xi[f]), ya[col + 1]));
+              if (gated) {
+                f0 *= silu(tc::bf16lo(zi[f]));
+                f1 *= silu(tc::bf16hi(zi[f]));
+              }
+              o[m][f] = tc::pack_bf16(f0, f1);
+            }
+          }
+          if (valid == L) {
+            tc::st_shared_v4(at0, o[0][0], o[0][1], o[0][2], o[0][3]);
+            tc::st_shared_v4(at1, o[1][0], o[1][1], o[1][2], o[1][3]);
+          } else if (t < valid) {
+            uint4* to = reinterpret_cast<uint4*>(yp + 16 * i);
+            to[0] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+            to[1] = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+          }
+          zr[0] = zn[0];
+          zr[1] = zn[1];
+        }
+        tc::tc_fence_before();
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(bar(YR));
       }
     }
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_relinquish();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(tmem, kTmem);
   }
   if (tid == 0 && *abort_flag) record_error(kErrTimeout);
 }
