@@ -9,13 +9,16 @@
 //   dy = q (w_post n' - y q^2 mean(w_post n' y)),  q = 1 / sqrt(mean(y^2) + eps)
 //   dw_post = sum_rows n' y q,  dw_pre = sum_rows x' h' r
 //
-// Bound by HBM.  A persistent CTA walks rows: the row's arrays arrive in shared memory by bulk
-// asynchronous copies a stage or more ahead (one mbarrier per stage), so the loads of the next
-// rows run under the two block-wide reductions of this one; a thread owns the same 8 K columns in
-// every row, so the fp32 vectors (and the backward's three column sums) stay in registers and are
-// read (written) once per CTA.  The column sums of the CTAs are added by a second kernel in a fixed
-// order, so the results are reproducible bit for bit.  Rows whose width is not a multiple of 8
-// values, or whose tensors are not 16-byte aligned, take the loop kernels at the end.
+// s and w_post meet one column sum A = sum_rows a SiLU(z) y q only: dw_post = s A, ds = w_post A.
+//
+// Bound by HBM.  One persistent CTA an SM, cut into groups of threads that walk rows of their own:
+// a row's arrays arrive in shared memory by bulk asynchronous copies a stage or more ahead (one
+// mbarrier per stage), and while one group waits for its block-wide sums another computes.  The fp32
+// vectors (w_post s, w_pre) sit in shared memory, read from HBM once per CTA; a thread owns the same
+// 8 K columns in every row, so the backward's two column sums stay in registers.  The sums of the
+// groups are added by a second kernel in a fixed order: reproducible bit for bit.  Rows whose width
+// is not a multiple of 8 values, or whose tensors are not 16-byte aligned, take the loop kernels at
+// the end.
 #pragma once
 
 #include "common.cuh"
@@ -38,44 +41,460 @@ struct BwdArgs {
   const void *y, *h, *z, *dh_in, *dx;     // h: the residual after the block
   const float *w_post, *w_pre, *scale;
   void *dy, *dh, *dz;
-  float* part;                            // [CTAs, 3, D]: dw_post, dw_pre, dscale
+  float* part;                            // [parts, 2, D]: A, dw_pre
   long rows;
   int D;
   float eps;
 };
 
-__device__ __forceinline__ float sigm(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
-
-// 8 consecutive values
-template <typename T> __device__ __forceinline__ void ld8(const T* p, float (&f)[8]);
-template <> __device__ __forceinline__ void ld8<float>(const float* p, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+// 1 / (1 + e^-v) from the hardware's 2^x and reciprocal (each within 2^-22)
+__device__ __forceinline__ float sigm(float v) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
 }
-template <>
-__device__ __forceinline__ void ld8<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+
+// 8 consecutive values as loaded, and as four pairs for the paired fp32 instructions
+template <typename T> struct Piece8;
+template <> struct Piece8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(f2_t (&f)[4]) const {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) f[i] = pk2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const f2_t (&f)[4]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x, y;
+      up2(f[i], x, y);
+      u[i] = tc::pack_bf16(x, y);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+template <> struct Piece8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(f2_t (&f)[4]) const {
+    f[0] = pk2(a.x, a.y);
+    f[1] = pk2(a.z, a.w);
+    f[2] = pk2(b.x, b.y);
+    f[3] = pk2(b.z, b.w);
+  }
+  static __device__ __forceinline__ void store(float* p, const f2_t (&f)[4]) {
+    float4 o[2];
+    up2(f[0], o[0].x, o[0].y);
+    up2(f[1], o[0].z, o[0].w);
+    up2(f[2], o[1].x, o[1].y);
+    up2(f[3], o[1].z, o[1].w);
+    reinterpret_cast<float4*>(p)[0] = o[0];
+    reinterpret_cast<float4*>(p)[1] = o[1];
+  }
+};
+__device__ __forceinline__ void ldv(const float* p, f2_t (&f)[4]) {   // 8 values of a vector
+  Piece8<float> v;
+  v.load(p);
+  v.get(f);
+}
+
+constexpr int kMaxGroups = 12, kMaxStages = 4;
+
+// A call's rows over the grid: `groups` groups of `nt` threads a CTA; group g of CTA b takes rows g gridDim.x + b,
+// then every (groups gridDim.x)-th.  The row stages: `n` arrays of a row each, `bytes[i]` long, at `at[i]` in a
+// stage; `off`: the same places by the array's role (a missing array has none).
+struct Ring {
+  const char* src[5];
+  uint32_t bytes[5], at[5], off[5];
+  uint32_t stage_bytes;
+  int n, stages, groups, nt;
+};
+
+__device__ __forceinline__ void group_sync(int g, int nt) {
+  if (nt == 32) __syncwarp();
+  else tc::named_bar(1 + g, nt);
+}
+
+// What both directions share: the barriers, the vectors in shared memory, and a group's row walk.
+struct Walk {
+  uint64_t* full;                // this group's stage barriers
+  unsigned char* stage0;         // this group's stages
+  int g, t;                      // group; thread in it
+  long row0, step, mine;         // first row, distance, number of rows
+  int st;                        // the present row's stage and its barrier's parity (counted, not divided)
+  uint32_t phase;
+  volatile int* abort_flag;
+
+  // `vec`: dynamic shared memory, [2][D] floats (w_post s, w_pre) and then the groups' stages
+  __device__ __forceinline__ void init(const Ring& ring, unsigned char* smem, uint64_t (*bars)[kMaxStages], int* abort_word,
+                                       const float* w_post, const float* scale, const float* w_pre, int D, long rows) {
+    abort_flag = abort_word;
+    g = threadIdx.x / ring.nt;
+    t = threadIdx.x % ring.nt;
+    full = bars[g];
+    stage0 = smem + 8L * D + (long)g * ring.stages * ring.stage_bytes;
+    if (threadIdx.x == 0) {
+      *abort_word = 0;
+      for (int i = 0; i < ring.groups; ++i)
+        for (int j = 0; j < ring.stages; ++j) tc::mbar_init(tc::smem_u32(&bars[i][j]), 1);
+      tc::fence_barrier_init();
+    }
+    row0 = (long)g * gridDim.x + blockIdx.x;
+    step = (long)ring.groups * gridDim.x;
+    mine = row0 < rows ? (rows - row0 + step - 1) / step : 0;
+    st = 0;
+    phase = 0;
+    __syncthreads();
+    if (t == 0)
+      for (int i = 0; i < ring.stages && i < mine; ++i) issue(ring, i, i);
+    float* v = reinterpret_cast<float*>(smem);
+    for (int c = threadIdx.x; c < D; c += blockDim.x) {
+      v[c] = (w_post ? w_post[c] : 1.f) * (scale ? scale[c] : 1.f);
+      v[D + c] = w_pre ? w_pre[c] : 1.f;
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void issue(const Ring& ring, long i, int to) const {   // row i into stage `to` (one thread)
+    const uint32_t bar = tc::smem_u32(&full[to]), dst = tc::smem_u32(stage0) + to * ring.stage_bytes;
+    tc::mbar_arrive_expect_tx(bar, ring.stage_bytes);
+    const long r = row0 + i * step;
+    for (int k = 0; k < ring.n; ++k)
+      tc::bulk_load(dst + ring.at[k], ring.src[k] + r * (long)ring.bytes[k], ring.bytes[k], bar);
+  }
+  __device__ __forceinline__ const unsigned char* wait(const Ring& ring) const {
+    tc::mbar_wait(tc::smem_u32(&full[st]), phase, abort_flag, kWaitCycles);
+    return stage0 + (uint32_t)st * ring.stage_bytes;
+  }
+  // after the first group-wide sync of row i: every thread holds the row in registers, its stage is free
+  __device__ __forceinline__ void refill(const Ring& ring, long i) {
+    if (t == 0 && i + ring.stages < mine) issue(ring, i + ring.stages, st);
+    if (++st == ring.stages) {
+      st = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Sum over the group; one sync.  `red` (32 floats) must not be in use by an earlier call that some
+// thread may still read.
+__device__ __forceinline__ float group_sum(float v, float* red, int g, int t, int nt) {
+  v = warp_sum(v);
+  if (nt == 32) {
+    __syncwarp();
+    return v;
+  }
+  if ((t & 31) == 0) red[t >> 5] = v;
+  group_sync(g, nt);
+  return warp_sum((t & 31) < (nt >> 5) ? red[t & 31] : 0.f);
+}
+// Four warp-wide sums in six shuffles: the halves, then the quarters of the warp each keep some of the values.  Lane
+// 8 i ends with the sum of v[i].
+__device__ __forceinline__ float warp_sum4(float4 v, int lane) {
+  const bool hi = lane & 16, odd = lane & 8;
+  const float a = (hi ? v.z : v.x) + __shfl_xor_sync(0xffffffffu, hi ? v.x : v.z, 16);
+  const float b = (hi ? v.w : v.y) + __shfl_xor_sync(0xffffffffu, hi ? v.y : v.w, 16);
+  float x = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// Three sums over the group; one sync.  red: [32][4] floats.
+__device__ __forceinline__ void group_sum3(float& p, float& q, float& r, float* red, int g, int t, int nt) {
+  const int lane = t & 31;
+  float x = warp_sum4(make_float4(p, q, r, 0.f), lane);
+  if (nt == 32) {
+    __syncwarp();
+  } else {
+    if ((lane & 7) == 0) red[(t >> 5) * 4 + (lane >> 3)] = x;
+    group_sync(g, nt);
+    x = warp_sum4(lane < (nt >> 5) ? reinterpret_cast<const float4*>(red)[lane] : make_float4(0.f, 0.f, 0.f, 0.f), lane);
+  }
+  p = __shfl_sync(0xffffffffu, x, 0);
+  q = __shfl_sync(0xffffffffu, x, 8);
+  r = __shfl_sync(0xffffffffu, x, 16);
+}
+
+// ---------------------------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------------------------
+template <typename T, typename TH, int K, int MAXT>
+__global__ void __launch_bounds__(MAXT) fwd_kernel(const FwdArgs a, const Ring ring) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[kMaxGroups][kMaxStages];
+  __shared__ float red[kMaxGroups][3][32];
+  __shared__ int abort_word;
+  Walk w;
+  w.init(ring, smem, bars, &abort_word, a.w_post, a.scale, a.w_pre, a.D, a.rows);
+  const float* sw = reinterpret_cast<const float*>(smem);
+  const float* wn = sw + a.D;
+  const int nt = ring.nt, t = w.t, g = w.g;
+  const float invD = 1.0f / (float)a.D;
+#pragma unroll 1
+  for (long i = 0; i < w.mine; ++i) {
+    const long at = (w.row0 + i * w.step) * a.D;
+    const unsigned char* base = w.wait(ring);
+    const T* sy = reinterpret_cast<const T*>(base + ring.off[0]);
+    const TH* sh = reinterpret_cast<const TH*>(base + ring.off[1]);
+    const T* sz = reinterpret_cast<const T*>(base + ring.off[2]);
+    Piece8<TH> hv[K];
+    Piece8<T> zv[K];
+    f2_t v[K][4];
+    f2_t q2 = 0;                       // (+0, +0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * nt + t) * 8;
+      Piece8<T> y;
+      y.zero();
+      hv[k].zero();
+      zv[k].zero();
+      if (c < a.D) {
+        y.load(sy + c);
+        hv[k].load(sh + c);
+        if (a.z) zv[k].load(sz + c);
+      }
+      y.get(v[k]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q2 = fma2(v[k][e], v[k][e], q2);
+    }
+    float ry = 1.f;
+    // without the second norm's sync the next row's sums go to the other buffer
+    if (a.w_post) ry = rsqrtf(fmaf(group_sum(hsum2(q2), red[g][a.w_pre ? 0 : (int)(i & 1)], g, t, nt), invD, a.eps));
+    else group_sync(g, nt);
+    w.refill(ring, i);
+    const f2_t ry2 = splat2(ry);
+    q2 = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * nt + t) * 8;
+      if (c < a.D) {
+        f2_t f[4], u[4];
+        if (a.z) {
+          zv[k].get(f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float z0, z1;
+            up2(f[e], z0, z1);
+            v[k][e] = mul2(v[k][e], mul2(f[e], pk2(sigm(z0), sigm(z1))));
+          }
+        }
+        ldv(sw + c, u);
+        hv[k].get(f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[k][e] = fma2(mul2(v[k][e], ry2), u[e], f[e]);
+          q2 = fma2(v[k][e], v[k][e], q2);
+        }
+        Piece8<TH>::store(static_cast<TH*>(a.h_out) + at + c, v[k]);
+      }
+    }
+    if (a.w_pre) {
+      const f2_t rh2 = splat2(rsqrtf(fmaf(group_sum(hsum2(q2), red[g][2], g, t, nt), invD, a.eps)));
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = (k * nt + t) * 8;
+        if (c < a.D) {
+          f2_t u[4];
+          ldv(wn + c, u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[k][e] = mul2(v[k][e], mul2(rh2, u[e]));
+          Piece8<T>::store(static_cast<T*>(a.x) + at + c, v[k]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_word) record_error(kErrTimeout);
+}
+
+// ---------------------------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------------------------
+template <typename T, typename TH, int K, int MAXT>
+__global__ void __launch_bounds__(MAXT) bwd_kernel(const BwdArgs a, const Ring ring) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[kMaxGroups][kMaxStages];
+  __shared__ __align__(16) float red3[kMaxGroups][128];
+  __shared__ float red1[kMaxGroups][32];
+  __shared__ int abort_word;
+  Walk w;
+  w.init(ring, smem, bars, &abort_word, a.w_post, a.scale, a.w_pre, a.D, a.rows);
+  const float* sw = reinterpret_cast<const float*>(smem);
+  const float* wn = sw + a.D;
+  const int nt = ring.nt, t = w.t, g = w.g;
+  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+  f2_t ga[K][4], gn[K][4];               // the column sums A and dw_pre over this group's rows
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ga[k][e] = gn[k][e] = 0;
+  const float invD = 1.0f / (float)a.D;
+#pragma unroll 1
+  for (long i = 0; i < w.mine; ++i) {
+    const long at = (w.row0 + i * w.step) * a.D;
+    const unsigned char* base = w.wait(ring);
+    Piece8<T> yv[K], zv[K], dx[K];
+    Piece8<TH> hv[K], dh[K];
+    // the three sums that do not need dh: y^2, h'^2, w_pre x' h'
+    f2_t qy = 0, qh = 0, qx = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * nt + t) * 8;
+      yv[k].zero();
+      zv[k].zero();
+      dx[k].zero();
+      hv[k].zero();
+      dh[k].zero();
+      if (c < a.D) {
+        yv[k].load(reinterpret_cast<const T*>(base + ring.off[0]) + c);
+        if (a.z) zv[k].load(reinterpret_cast<const T*>(base + ring.off[2]) + c);
+        if (a.dh_in) dh[k].load(reinterpret_cast<const TH*>(base + ring.off[3]) + c);
+        f2_t f[4];
+        yv[k].get(f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qy = fma2(f[e], f[e], qy);
+        if (pre) {
+          hv[k].load(reinterpret_cast<const TH*>(base + ring.off[1]) + c);
+          dx[k].load(reinterpret_cast<const T*>(base + ring.off[4]) + c);
+          f2_t d[4], u[4];
+          hv[k].get(f);
+          dx[k].get(d);
+          ldv(wn + c, u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            qh = fma2(f[e], f[e], qh);
+            qx = fma2(mul2(f[e], u[e]), d[e], qx);
+          }
+        }
+      }
+    }
+    float sy = hsum2(qy), sh = hsum2(qh), sx = hsum2(qx);
+    group_sum3(sy, sh, sx, red3[g], g, t, nt);
+    w.refill(ring, i);
+    const float ry = post ? rsqrtf(fmaf(sy, invD, a.eps)) : 1.f;
+    const float rh = pre ? rsqrtf(fmaf(sh, invD, a.eps)) : 0.f;
+    const f2_t ry2 = splat2(ry), rh2 = splat2(rh), mx2 = splat2(-rh * rh * sx * invD);
+    const f2_t one = splat2(1.f), minus = splat2(-1.f);
+    f2_t u[K][4];                        // n' w_post: what dy starts from
+    f2_t qd = 0;                         // w_post n' y
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * nt + t) * 8;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[k][e] = 0;
+      if (c < a.D) {
+        f2_t d[4], y[4], f[4], v[4];
+        dh[k].get(d);
+        if (pre) {
+          hv[k].get(f);
+          dx[k].get(v);
+          ldv(wn + c, y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            gn[k][e] = fma2(mul2(v[e], rh2), f[e], gn[k][e]);
+            d[e] = fma2(rh2, fma2(v[e], y[e], mul2(f[e], mx2)), d[e]);
+          }
+        }
+        Piece8<TH>::store(static_cast<TH*>(a.dh) + at + c, d);
+        yv[k].get(y);
+        ldv(sw + c, v);
+        if (a.z) {
+          f2_t z[4];
+          zv[k].get(z);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float z0, z1;
+            up2(z[e], z0, z1);
+            const f2_t s = pk2(sigm(z0), sigm(z1)), gate = mul2(z[e], s);
+            const f2_t yr = mul2(y[e], ry2), as = mul2(d[e], v[e]);
+            f[e] = mul2(mul2(as, yr), mul2(s, fma2(z[e], fma2(s, minus, one), one)));
+            ga[k][e] = fma2(mul2(d[e], gate), yr, ga[k][e]);
+            u[k][e] = mul2(as, gate);
+            qd = fma2(u[k][e], y[e], qd);
+          }
+          Piece8<T>::store(static_cast<T*>(a.dz) + at + c, f);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ga[k][e] = fma2(d[e], mul2(y[e], ry2), ga[k][e]);
+            u[k][e] = mul2(d[e], v[e]);
+            qd = fma2(u[k][e], y[e], qd);
+          }
+        }
+      }
+    }
+    if (post) {
+      const float my = ry * ry * group_sum(hsum2(qd), red1[g], g, t, nt) * invD;
+      const f2_t my2 = splat2(-ry * my);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        f2_t y[4];
+        yv[k].get(y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[k][e] = fma2(y[e], my2, mul2(u[k][e], ry2));
+      }
+    } else {
+      group_sync(g, nt);                 // red3 is written again in the next row
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * nt + t) * 8;
+      if (c < a.D) Piece8<T>::store(static_cast<T*>(a.dy) + at + c, u[k]);
+    }
+  }
+  float* part = a.part + ((long)blockIdx.x * ring.groups + g) * 2 * a.D;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * nt + t) * 8;
+    if (c < a.D) {
+      Piece8<float>::store(part + c, ga[k]);
+      Piece8<float>::store(part + a.D + c, gn[k]);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_word) record_error(kErrTimeout);
+}
+
+// Column sums of the parts, in a fixed order: 32 columns x 16 slices of the parts per block, then
+// the 16 slices.  blockIdx.y: A (giving dw_post and dscale) or dw_pre.
+__global__ void __launch_bounds__(512) column_sum_kernel(const float* __restrict__ part, int parts, int D,
+                                                         const float* __restrict__ w_post, const float* __restrict__ scale,
+                                                         float* dw_post, float* dw_pre, float* dscale) {
+  __shared__ float s[16][33];
+  if (blockIdx.y == 0 ? !dw_post && !dscale : !dw_pre) return;
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < D) {
+    const float* p = part + (long)blockIdx.y * D + c;
+#pragma unroll 4
+    for (int i = slice; i < parts; i += 16) v += p[(long)i * 2 * D];
+  }
+  s[slice][lane] = v;
+  __syncthreads();
+  if (slice == 0 && c < D) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += s[i][lane];
+    if (blockIdx.y == 1) {
+      dw_pre[c] = t;
+    } else {
+      if (dw_post) dw_post[c] = t * (scale ? scale[c] : 1.f);
+      if (dscale) dscale[c] = t * (w_post ? w_post[c] : 1.f);
+    }
   }
 }
-template <typename T> __device__ __forceinline__ void st8(T* p, const float (&f)[8]);
-template <> __device__ __forceinline__ void st8<float>(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-template <>
-__device__ __forceinline__ void st8<__nv_bfloat16>(__nv_bfloat16* p, const float (&f)[8]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) u[i] = tc::pack_bf16(f[2 * i], f[2 * i + 1]);
-  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-}
 
+// ---------------------------------------------------------------------------------------------
+// any width and alignment: the row is read again in each pass (from L1 / L2)
+// ---------------------------------------------------------------------------------------------
 // Sum over the CTA; one barrier: `red` (32 floats) must not be in use by an earlier call that some
 // thread may still read, so callers alternate between two.
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -91,340 +510,6 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
-// The row stages: `n` arrays of a row each, `bytes[i]` long, at `at[i]` in a stage; `off`: the same
-// places by the array's role (a missing array has none).
-struct Ring {
-  const char* src[5];
-  uint32_t bytes[5], at[5], off[5];
-  uint32_t stage_bytes;
-  int n, stages;
-};
-
-// ---------------------------------------------------------------------------------------------
-// forward
-// ---------------------------------------------------------------------------------------------
-template <typename T, typename TH, int K, int MAXT>
-__global__ void __launch_bounds__(MAXT) fwd_kernel(const FwdArgs a, const Ring ring) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ __align__(8) uint64_t full[4];
-  __shared__ float red[3][32];
-  __shared__ int abort_word;
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const uint32_t sb = tc::smem_u32(smem);
-  volatile int* abort_flag = &abort_word;
-  if (tid == 0) {
-    abort_word = 0;
-    for (int i = 0; i < ring.stages; ++i) tc::mbar_init(tc::smem_u32(&full[i]), 1);
-    tc::fence_barrier_init();
-  }
-  __syncthreads();
-  const long row0 = blockIdx.x, step = gridDim.x;
-  const long mine = row0 < a.rows ? (a.rows - row0 + step - 1) / step : 0;
-  auto issue = [&](long i) {             // this CTA's i-th row into its stage (one thread)
-    const int st = (int)(i % ring.stages);
-    const uint32_t bar = tc::smem_u32(&full[st]), dst = sb + st * ring.stage_bytes;
-    tc::mbar_arrive_expect_tx(bar, ring.stage_bytes);
-    const long r = row0 + i * step;
-    for (int k = 0; k < ring.n; ++k)
-      tc::bulk_load(dst + ring.at[k], ring.src[k] + r * (long)ring.bytes[k], ring.bytes[k], bar);
-  };
-  if (tid == 0)
-    for (long i = 0; i < ring.stages && i < mine; ++i) issue(i);
-
-  float wp[K][8], wn[K][8], sc[K][8];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (k * nt + tid) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) wp[k][e] = sc[k][e] = wn[k][e] = 1.f;
-    if (c < a.D) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (a.w_post) wp[k][e] = a.w_post[c + e];
-        if (a.w_pre) wn[k][e] = a.w_pre[c + e];
-        if (a.scale) sc[k][e] = a.scale[c + e];
-      }
-    }
-  }
-  const float invD = 1.0f / (float)a.D;
-  for (long i = 0; i < mine; ++i) {
-    const int st = (int)(i % ring.stages);
-    const long r = row0 + i * step;
-    const unsigned char* base = smem + (long)st * ring.stage_bytes;
-    const T* sy = reinterpret_cast<const T*>(base + ring.off[0]);
-    const TH* sh = reinterpret_cast<const TH*>(base + ring.off[1]);
-    const T* sz = reinterpret_cast<const T*>(base + ring.off[2]);
-    tc::mbar_wait(tc::smem_u32(&full[st]), (uint32_t)(i / ring.stages) & 1u, abort_flag, kWaitCycles);
-    float v[K][8];
-    float q = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * nt + tid) * 8;
-      if (c < a.D) ld8<T>(sy + c, v[k]);
-      else for (int e = 0; e < 8; ++e) v[k][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q = fmaf(v[k][e], v[k][e], q);
-    }
-    float ry = 1.f;
-    // without the second norm's barrier the next row's sums go to the other buffer
-    if (a.w_post) ry = rsqrtf(fmaf(block_sum(q, red[a.w_pre ? 0 : (int)(i & 1)]), invD, a.eps));
-    else __syncthreads();
-    // every thread has left the previous row's stage: refill it
-    if (ring.stages > 1 && tid == 0 && i > 0 && i - 1 + ring.stages < mine) issue(i - 1 + ring.stages);
-    q = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * nt + tid) * 8;
-      float hv[8];
-      if (c < a.D) ld8<TH>(sh + c, hv);
-      else for (int e = 0; e < 8; ++e) hv[e] = 0.f;
-      if (a.z) {
-        float zv[8];
-        if (c < a.D) ld8<T>(sz + c, zv);
-        else for (int e = 0; e < 8; ++e) zv[e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] *= zv[e] * sigm(zv[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[k][e] = fmaf(v[k][e] * ry, wp[k][e] * sc[k][e], hv[e]);
-        q = fmaf(v[k][e], v[k][e], q);
-      }
-      if (c < a.D) st8<TH>(static_cast<TH*>(a.h_out) + r * a.D + c, v[k]);
-    }
-    if (a.w_pre) {
-      const float rh = rsqrtf(fmaf(block_sum(q, red[2]), invD, a.eps));
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = (k * nt + tid) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] *= rh * wn[k][e];
-        if (c < a.D) st8<T>(static_cast<T*>(a.x) + r * a.D + c, v[k]);
-      }
-    }
-    if (ring.stages == 1) {
-      __syncthreads();
-      if (tid == 0 && i + 1 < mine) issue(i + 1);
-    }
-  }
-  __syncthreads();
-  if (tid == 0 && abort_word) record_error(kErrTimeout);
-}
-
-// ---------------------------------------------------------------------------------------------
-// backward
-// ---------------------------------------------------------------------------------------------
-template <typename T, typename TH, int K, int MAXT>
-__global__ void __launch_bounds__(MAXT) bwd_kernel(const BwdArgs a, const Ring ring) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ __align__(8) uint64_t full[4];
-  __shared__ float red[4][32];
-  __shared__ int abort_word;
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const uint32_t sb = tc::smem_u32(smem);
-  volatile int* abort_flag = &abort_word;
-  if (tid == 0) {
-    abort_word = 0;
-    for (int i = 0; i < ring.stages; ++i) tc::mbar_init(tc::smem_u32(&full[i]), 1);
-    tc::fence_barrier_init();
-  }
-  __syncthreads();
-  const long row0 = blockIdx.x, step = gridDim.x;
-  const long mine = row0 < a.rows ? (a.rows - row0 + step - 1) / step : 0;
-  auto issue = [&](long i) {
-    const int st = (int)(i % ring.stages);
-    const uint32_t bar = tc::smem_u32(&full[st]), dst = sb + st * ring.stage_bytes;
-    tc::mbar_arrive_expect_tx(bar, ring.stage_bytes);
-    const long r = row0 + i * step;
-    for (int k = 0; k < ring.n; ++k)
-      tc::bulk_load(dst + ring.at[k], ring.src[k] + r * (long)ring.bytes[k], ring.bytes[k], bar);
-  };
-  if (tid == 0)
-    for (long i = 0; i < ring.stages && i < mine; ++i) issue(i);
-
-  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
-  // the three vectors and their gradients' sums over this CTA's rows
-  float wp[K][8], wn[K][8], sc[K][8], gp[K][8], gn[K][8], gs[K][8];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (k * nt + tid) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      wp[k][e] = wn[k][e] = sc[k][e] = 1.f;
-      gp[k][e] = gn[k][e] = gs[k][e] = 0.f;
-      if (c < a.D) {
-        if (post) wp[k][e] = a.w_post[c + e];
-        if (pre) wn[k][e] = a.w_pre[c + e];
-        if (a.scale) sc[k][e] = a.scale[c + e];
-      }
-    }
-  }
-  const float invD = 1.0f / (float)a.D;
-  for (long i = 0; i < mine; ++i) {
-    const int st = (int)(i % ring.stages);
-    const long r = row0 + i * step;
-    const unsigned char* base = smem + (long)st * ring.stage_bytes;
-    const T* sy = reinterpret_cast<const T*>(base + ring.off[0]);
-    const TH* sh = reinterpret_cast<const TH*>(base + ring.off[1]);
-    const T* sz = reinterpret_cast<const T*>(base + ring.off[2]);
-    const TH* sg = reinterpret_cast<const TH*>(base + ring.off[3]);
-    const T* sx = reinterpret_cast<const T*>(base + ring.off[4]);
-    tc::mbar_wait(tc::smem_u32(&full[st]), (uint32_t)(i / ring.stages) & 1u, abort_flag, kWaitCycles);
-    // the three sums that do not need dh: y^2, h'^2, w_pre x' h'
-    float qy = 0.f, qh = 0.f, qx = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * nt + tid) * 8;
-      if (c < a.D) {
-        float f[8];
-        if (post) {
-          ld8<T>(sy + c, f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) qy = fmaf(f[e], f[e], qy);
-        }
-        if (pre) {
-          float d[8];
-          ld8<TH>(sh + c, f);
-          ld8<T>(sx + c, d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            qh = fmaf(f[e], f[e], qh);
-            qx = fmaf(f[e] * wn[k][e], d[e], qx);
-          }
-        }
-      }
-    }
-    qy = warp_sum(qy);
-    qh = warp_sum(qh);
-    qx = warp_sum(qx);
-    const int warps = (nt + 31) >> 5, lane = tid & 31;
-    if (lane == 0) {
-      red[0][tid >> 5] = qy;
-      red[1][tid >> 5] = qh;
-      red[2][tid >> 5] = qx;
-    }
-    __syncthreads();
-    if (ring.stages > 1 && tid == 0 && i > 0 && i - 1 + ring.stages < mine) issue(i - 1 + ring.stages);
-    qy = warp_sum(lane < warps ? red[0][lane] : 0.f);
-    qh = warp_sum(lane < warps ? red[1][lane] : 0.f);
-    qx = warp_sum(lane < warps ? red[2][lane] : 0.f);
-    const float ry = post ? rsqrtf(fmaf(qy, invD, a.eps)) : 1.f;
-    const float rh = pre ? rsqrtf(fmaf(qh, invD, a.eps)) : 0.f;
-    const float mx = rh * rh * qx * invD;
-    float u[K][8];                       // n' w_post: what dy starts from
-    float qd = 0.f;                      // w_post n' y
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * nt + tid) * 8;
-      if (c < a.D) {
-        float yv[8], dh[8], f[8];
-        ld8<T>(sy + c, yv);
-        if (a.dh_in) ld8<TH>(sg + c, dh);
-        else for (int e = 0; e < 8; ++e) dh[e] = 0.f;
-        if (pre) {
-          float d[8];
-          ld8<TH>(sh + c, f);
-          ld8<T>(sx + c, d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            gn[k][e] = fmaf(d[e] * rh, f[e], gn[k][e]);
-            dh[e] = fmaf(rh, fmaf(d[e], wn[k][e], -f[e] * mx), dh[e]);
-          }
-        }
-        st8<TH>(static_cast<TH*>(a.dh) + r * a.D + c, dh);
-        if (a.z) {
-          float zv[8], dz[8];
-          ld8<T>(sz + c, zv);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float s = sigm(zv[e]), gate = zv[e] * s;
-            const float yr = yv[e] * ry, as = dh[e] * sc[k][e];
-            const float n = yr * wp[k][e];
-            gs[k][e] = fmaf(dh[e] * gate, n, gs[k][e]);
-            dz[e] = as * n * s * fmaf(zv[e], 1.f - s, 1.f);
-            const float dn = as * gate;
-            gp[k][e] = fmaf(dn, yr, gp[k][e]);
-            u[k][e] = dn * wp[k][e];
-            qd = fmaf(u[k][e], yv[e], qd);
-          }
-          st8<T>(static_cast<T*>(a.dz) + r * a.D + c, dz);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float yr = yv[e] * ry, dn = dh[e] * sc[k][e];
-            gs[k][e] = fmaf(dh[e], yr * wp[k][e], gs[k][e]);
-            gp[k][e] = fmaf(dn, yr, gp[k][e]);
-            u[k][e] = dn * wp[k][e];
-            qd = fmaf(u[k][e], yv[e], qd);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[k][e] = 0.f;
-      }
-    }
-    float my = 0.f;
-    if (post) my = ry * ry * block_sum(qd, red[3]) * invD;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * nt + tid) * 8;
-      if (c < a.D) {
-        if (post) {
-          float yv[8];
-          ld8<T>(sy + c, yv);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[k][e] = ry * fmaf(-yv[e], my, u[k][e]);
-        }
-        st8<T>(static_cast<T*>(a.dy) + r * a.D + c, u[k]);
-      }
-    }
-    if (!post || ring.stages == 1) {      // red[0..2] and the stage are used again
-      __syncthreads();
-      if (ring.stages == 1 && tid == 0 && i + 1 < mine) issue(i + 1);
-    }
-  }
-  float* part = a.part + (long)blockIdx.x * 3 * a.D;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (k * nt + tid) * 8;
-    if (c < a.D) {
-      if (post) st8<float>(part + c, gp[k]);
-      if (pre) st8<float>(part + (long)a.D + c, gn[k]);
-      if (a.scale) st8<float>(part + 2L * a.D + c, gs[k]);
-    }
-  }
-  __syncthreads();
-  if (tid == 0 && abort_word) record_error(kErrTimeout);
-}
-
-// Column sums of the CTAs' parts, in a fixed order: 32 columns x 16 slices of the CTAs per block,
-// then the 16 slices.  blockIdx.y: which of the three vectors.
-__global__ void __launch_bounds__(512) column_sum_kernel(const float* __restrict__ part, int ctas, int D,
-                                                         float* dw_post, float* dw_pre, float* dscale) {
-  __shared__ float s[16][33];
-  float* out = blockIdx.y == 0 ? dw_post : blockIdx.y == 1 ? dw_pre : dscale;
-  if (!out) return;
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < D) {
-    const float* p = part + (long)blockIdx.y * D + c;
-#pragma unroll 4
-    for (int i = slice; i < ctas; i += 16) v += p[(long)i * 3 * D];
-  }
-  s[slice][lane] = v;
-  __syncthreads();
-  if (slice == 0 && c < D) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t += s[i][lane];
-    out[c] = t;
-  }
-}
-
-// ---------------------------------------------------------------------------------------------
-// any width and alignment: the row is read again in each pass (from L1 / L2)
-// ---------------------------------------------------------------------------------------------
 constexpr int kLoopThreads = 256;
 
 template <typename T, typename TH>
@@ -477,9 +562,9 @@ __global__ void __launch_bounds__(kLoopThreads) bwd_loop_kernel(const BwdArgs a)
   const int tid = threadIdx.x;
   const float invD = 1.0f / (float)a.D;
   const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
-  float* gp = a.part + (long)blockIdx.x * 3 * a.D;
-  float *gn = gp + a.D, *gs = gn + a.D;
-  for (int c = tid; c < a.D; c += kLoopThreads) gp[c] = gn[c] = gs[c] = 0.f;
+  float* ga = a.part + (long)blockIdx.x * 2 * a.D;
+  float* gn = ga + a.D;
+  for (int c = tid; c < a.D; c += kLoopThreads) ga[c] = gn[c] = 0.f;
   for (long r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* y = static_cast<const T*>(a.y) + r * a.D;
     const TH* h = static_cast<const TH*>(a.h) + r * a.D;
@@ -531,8 +616,7 @@ __global__ void __launch_bounds__(kLoopThreads) bwd_loop_kernel(const BwdArgs a)
         gate = zv * s;
         dzo[c] = from_f<T>(dh * (a.scale ? a.scale[c] : 1.f) * n * s * fmaf(zv, 1.f - s, 1.f));
       }
-      gp[c] = fmaf(dn, yr, gp[c]);
-      gs[c] = fmaf(dh * gate, n, gs[c]);
+      ga[c] = fmaf(dh * gate, yr, ga[c]);
       if (pre) gn[c] = fmaf(to_f(dx[c]) * rh, to_f(h[c]), gn[c]);
       if (post) qd = fmaf(dn * w, to_f(y[c]), qd);
       else dyo[c] = from_f<T>(dn);

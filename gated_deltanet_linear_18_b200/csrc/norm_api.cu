@@ -10,29 +10,38 @@ using namespace gdn;
 namespace {
 
 constexpr int kSms = 148;
-constexpr uint32_t kStageBytes = 200 * 1024;   // shared memory of an SM given to row stages
+constexpr uint32_t kSmem = 216 * 1024;   // shared memory of a CTA given to vectors and row stages
 
 bool elem_aligned(const void* p, size_t el) { return (reinterpret_cast<uintptr_t>(p) & (el - 1)) == 0; }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// How a width is walked: `k` pieces of 8 columns a thread, `threads` threads, `ctas` per SM.
+// How a width is walked: `k` pieces of 8 columns a thread, groups of `nt` threads, `groups` a CTA and
+// `stages` row stages a group.
 struct Shape {
-  int k, threads, ctas;
+  int k, nt, groups, stages;
 };
-// One piece a thread up to 2048 columns, two up to 8192 (512 threads); enough CTAs on an SM to
-// give it about 512 threads.
-Shape shape_of(int D) {
-  const int nv = D / 8, k = nv <= 256 ? 1 : 2;
-  const int threads = ((nv + k - 1) / k + 31) / 32 * 32;
-  return Shape{k, threads, std::max(1, std::min(8, 512 / threads))};
+// One piece a thread up to 2048 columns, two above; as many groups as make 768 threads (512 where the
+// backward's two pieces fill the registers), fewer where a row stage for each does not fit beside the
+// vectors.  groups = 0: the width is not walked.
+int pieces(int D) { return D <= 2048 ? 1 : 2; }
+int group_threads(int D) { return ((D / 8 + pieces(D) - 1) / pieces(D) + 31) / 32 * 32; }
+int most_groups(int D, bool backward) {
+  return std::max(1, std::min(bn::kMaxGroups, (backward && pieces(D) == 2 ? 512 : 768) / group_threads(D)));
 }
-bool ring_fits(int D, uint32_t row_bytes) {
-  return D % 8 == 0 && D <= 8192 && row_bytes <= kStageBytes / shape_of(D).ctas;
+Shape shape_of(int D, uint32_t row_bytes, bool backward) {
+  if (D % 8 != 0 || D > 8192) return Shape{0, 0, 0, 0};
+  const uint32_t room = kSmem - 8u * D;
+  int groups = most_groups(D, backward);
+  while (groups > 1 && room / (groups * row_bytes) < 1) --groups;
+  const int stages = (int)std::min<uint32_t>(bn::kMaxStages, room / (groups * row_bytes));
+  return stages < 1 ? Shape{0, 0, 0, 0} : Shape{pieces(D), group_threads(D), groups, stages};
 }
-// CTAs of the backward: as many as run at once, at most one per row; the loop kernel's walk four a SM.
-long bwd_ctas(long rows, int D) {
-  const int per = D % 8 == 0 && D <= 8192 ? shape_of(D).ctas : 4;
-  return std::min<long>(rows, (long)kSms * per);
+// Parts of the backward's column sums that the workspace holds: the most of its two kernels, each of which
+// writes one a group or CTA.
+constexpr int kLoopCtas = kSms * 4;
+long bwd_parts(long rows, int D) {
+  const long walked = D % 8 == 0 && D <= 8192 ? std::min<long>(rows, kSms) * most_groups(D, true) : 0;
+  return std::max(walked, std::min<long>(rows, kLoopCtas));
 }
 
 void ring_add(bn::Ring& r, int i, const void* p, uint32_t bytes) {
@@ -46,12 +55,14 @@ void ring_add(bn::Ring& r, int i, const void* p, uint32_t bytes) {
 }
 
 template <typename Kern, typename Args>
-gdn_status launch_ring(Kern kern, const Args& a, bn::Ring ring, const Shape& s, long ctas, cudaStream_t st) {
-  ring.stages = (int)std::min<uint32_t>(4, kStageBytes / s.ctas / ring.stage_bytes);
-  const uint32_t smem = ring.stages * ring.stage_bytes;
+gdn_status launch_ring(Kern kern, const Args& a, bn::Ring ring, const Shape& s, cudaStream_t st) {
+  ring.stages = s.stages;
+  ring.groups = s.groups;
+  ring.nt = s.nt;
+  const uint32_t smem = 8u * a.D + s.groups * s.stages * ring.stage_bytes;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return GDN_ERR_CUDA;
-  kern<<<(unsigned)ctas, s.threads, smem, st>>>(a, ring);
+  kern<<<(unsigned)std::min<long>(a.rows, kSms), s.groups * s.nt, smem, st>>>(a, ring);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -59,48 +70,50 @@ template <typename T, typename TH>
 gdn_status fwd(const bn::FwdArgs& a, bool vec, cudaStream_t st) {
   bn::Ring ring{};
   const uint32_t bt = (uint32_t)a.D * sizeof(T), bh = (uint32_t)a.D * sizeof(TH);
+  Shape s{0, 0, 0, 0};
   if (vec) {
     ring_add(ring, 0, a.y, bt);
     ring_add(ring, 1, a.h, bh);
     ring_add(ring, 2, a.z, bt);
+    s = shape_of(a.D, ring.stage_bytes, false);
   }
-  if (!vec || !ring_fits(a.D, ring.stage_bytes)) {
+  if (s.groups == 0) {
     bn::fwd_loop_kernel<T, TH><<<(unsigned)std::min<long>(a.rows, kSms * 8), bn::kLoopThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
   }
-  const Shape s = shape_of(a.D);
-  const long ctas = std::min<long>(a.rows, (long)kSms * s.ctas);
-  if (s.k == 1) return launch_ring(bn::fwd_kernel<T, TH, 1, 256>, a, ring, s, ctas, st);
-  if (s.threads <= 384) return launch_ring(bn::fwd_kernel<T, TH, 2, 384>, a, ring, s, ctas, st);
-  return launch_ring(bn::fwd_kernel<T, TH, 2, 512>, a, ring, s, ctas, st);
+  if (s.k == 1) return launch_ring(bn::fwd_kernel<T, TH, 1, 768>, a, ring, s, st);
+  return launch_ring(bn::fwd_kernel<T, TH, 2, 768>, a, ring, s, st);
 }
 
 template <typename T, typename TH>
 gdn_status bwd(const bn::BwdArgs& a, bool vec, float* dw_post, float* dw_pre, float* dscale, cudaStream_t st) {
   bn::Ring ring{};
   const uint32_t bt = (uint32_t)a.D * sizeof(T), bh = (uint32_t)a.D * sizeof(TH);
+  Shape sh{0, 0, 0, 0};
   if (vec) {
     ring_add(ring, 0, a.y, bt);
     ring_add(ring, 1, a.w_pre ? a.h : nullptr, bh);
     ring_add(ring, 2, a.z, bt);
     ring_add(ring, 3, a.dh_in, bh);
     ring_add(ring, 4, a.w_pre ? a.dx : nullptr, bt);
+    sh = shape_of(a.D, ring.stage_bytes, true);
   }
-  const long ctas = bwd_ctas(a.rows, a.D);
   gdn_status s = GDN_OK;
-  if (!vec || !ring_fits(a.D, ring.stage_bytes)) {
-    bn::bwd_loop_kernel<T, TH><<<(unsigned)ctas, bn::kLoopThreads, 0, st>>>(a);
+  long parts;
+  if (sh.groups == 0) {
+    parts = std::min<long>(a.rows, kLoopCtas);
+    bn::bwd_loop_kernel<T, TH><<<(unsigned)parts, bn::kLoopThreads, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) s = GDN_ERR_CUDA;
   } else {
-    const Shape sh = shape_of(a.D);
-    s = sh.k == 1 ? launch_ring(bn::bwd_kernel<T, TH, 1, 256>, a, ring, sh, ctas, st)
-        : sh.threads <= 384 ? launch_ring(bn::bwd_kernel<T, TH, 2, 384>, a, ring, sh, ctas, st)
-                            : launch_ring(bn::bwd_kernel<T, TH, 2, 512>, a, ring, sh, ctas, st);
+    parts = std::min<long>(a.rows, kSms) * sh.groups;
+    s = sh.k == 1                    ? launch_ring(bn::bwd_kernel<T, TH, 1, 768>, a, ring, sh, st)
+        : sh.groups * sh.nt <= 384 ? launch_ring(bn::bwd_kernel<T, TH, 2, 384>, a, ring, sh, st)
+                                   : launch_ring(bn::bwd_kernel<T, TH, 2, 512>, a, ring, sh, st);
   }
   if (s != GDN_OK) return s;
   if (!dw_post && !dw_pre && !dscale) return GDN_OK;
-  bn::column_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 3), 512, 0, st>>>(a.part, (int)ctas, a.D, dw_post,
-                                                                             dw_pre, dscale);
+  bn::column_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32), 2), 512, 0, st>>>(a.part, (int)parts, a.D, a.w_post, a.scale,
+                                                                             dw_post, dw_pre, dscale);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -147,7 +160,7 @@ gdn_status gdn_block_norm(const void* y, const void* h, const void* z, const flo
 
 size_t gdn_block_norm_bwd_workspace_bytes(long long rows, int D) {
   if (rows <= 0 || D <= 0) return 0;
-  return (size_t)bwd_ctas(rows, D) * 3 * D * sizeof(float);
+  return (size_t)bwd_parts(rows, D) * 2 * D * sizeof(float);
 }
 
 gdn_status gdn_block_norm_bwd(const void* y, const void* h_out, const void* z, const void* dh_out, const void* dx,

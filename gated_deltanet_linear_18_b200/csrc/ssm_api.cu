@@ -23,22 +23,22 @@ gdn_status launch_status() { return cudaGetLastError() == cudaSuccess ? GDN_OK :
 // ---------------------------------------------------------------------------------------------
 // convolution
 // ---------------------------------------------------------------------------------------------
-template <typename T, int VEC, int R>
-gdn_status conv_launch(const ssm::ConvArgs& a, cudaStream_t st) {
-  const long rows = a.cu ? (long)a.T : (long)a.nseq * a.T;
-  const long tiles = (rows + R - 1) / R + 1;
-  const long per = (long)ssm::kConvThreads * VEC, blocks = (a.C + per - 1) / per;
-  if (tiles > 0x7fffffffL || blocks > 65535) return GDN_ERR_UNSUPPORTED;
-  ssm::conv_kernel<T, VEC, R><<<dim3((unsigned)tiles, (unsigned)blocks), ssm::kConvThreads, 0, st>>>(a);
-  return launch_status();
-}
 template <typename T, int VEC>
-gdn_status conv_rows(const ssm::ConvArgs& a, cudaStream_t st) {
-  // 32 rows a thread where that still gives every SM 1024 threads, else 8: a short call needs the
-  // parallelism more than the 3 / R re-read of the window costs
+gdn_status conv_launch(ssm::ConvArgs a, cudaStream_t st) {
   const long rows = a.cu ? (long)a.T : (long)a.nseq * a.T;
-  if (rows * (a.C / VEC) >= 148L * 1024 * 32) return conv_launch<T, VEC, 32>(a, st);
-  return conv_launch<T, VEC, 8>(a, st);
+  const long per = (long)ssm::kConvThreads * VEC, blocks = (a.C + per - 1) / per;
+  if (blocks > 65535) return GDN_ERR_UNSUPPORTED;
+  // one wave of four CTAs an SM (128 registers), at least eight rows a thread
+  const long wave = 148L * 4 / blocks;
+  long tile = wave > 0 ? (rows + wave - 1) / wave : rows;
+  tile = (std::max(8L, tile) + ssm::kConvBatch - 1) / ssm::kConvBatch * ssm::kConvBatch;
+  tile = std::min(tile, 4096L);
+  const long tiles = (rows + tile - 1) / tile + 1;
+  if (tiles > 0x7fffffffL) return GDN_ERR_UNSUPPORTED;
+  a.tile = (int)tile;
+  a.w_vec = aligned(a.w, 16) && aligned(a.bias, 16);
+  ssm::conv_kernel<T, VEC><<<dim3((unsigned)tiles, (unsigned)blocks), ssm::kConvThreads, 0, st>>>(a);
+  return launch_status();
 }
 
 gdn_status conv_call(const void* x, long long ldx, const float* w, const float* bias, const void* hist_in, void* out,
@@ -56,10 +56,10 @@ gdn_status conv_call(const void* x, long long ldx, const float* w, const float* 
   const int v = dtype == GDN_F32 ? 4 : 8;
   const bool vec = C % v == 0 && ldx % v == 0 && aligned(x, 16) && aligned(out, 16) && aligned(hist_in, 16) &&
                    aligned(hist_out, 16);
-  const ssm::ConvArgs a{x, (long)ldx, w, bias, hist_in, out, hist_out, cu, nseq, T, max_len, C};
+  const ssm::ConvArgs a{x, (long)ldx, w, bias, hist_in, out, hist_out, cu, nseq, T, max_len, C, 0, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == GDN_F32) return vec ? conv_rows<float, 4>(a, st) : conv_rows<float, 1>(a, st);
-  return vec ? conv_rows<bf, 8>(a, st) : conv_rows<bf, 1>(a, st);
+  if (dtype == GDN_F32) return vec ? conv_launch<float, 4>(a, st) : conv_launch<float, 1>(a, st);
+  return vec ? conv_launch<bf, 8>(a, st) : conv_launch<bf, 1>(a, st);
 }
 
 // ---------------------------------------------------------------------------------------------

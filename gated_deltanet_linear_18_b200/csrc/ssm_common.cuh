@@ -10,13 +10,14 @@ namespace ssm {
 __device__ __forceinline__ float softplus(float v) {
   return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
 }
-// v / (1 + e^-v) from the hardware's 2^x and reciprocal (each within 2^-22; results below 2^-126 flush to 0)
-__device__ __forceinline__ float silu(float v) {
+// 1 / (1 + e^-v) from the hardware's 2^x and reciprocal (each within 2^-22; below 2^-126 it is 0)
+__device__ __forceinline__ float sigmoid(float v) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return v * r;
+  return r;
 }
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 
 // One call of the scan.  Token tensors have `ld*` values between tokens; inside a token's row the
 // heads (groups) follow one another without gaps.

@@ -3,11 +3,13 @@
 // with the three rows before the sequence taken from a carried history (zeros without one), and
 // the last three raw rows written out as the history after the call.
 //
-// Bound by HBM: each raw row is read once and each result written once (the 12 operations and two
-// special-function calls per value stay below that).  One thread owns VEC neighbouring channels
-// (16 bytes) and R consecutive rows: its taps and the three-row window stay in registers, and the
-// loads of kConvBatch rows are issued together before any of them is used.  Only the window's
-// three rows are read twice (3 / R more reads, from L2).
+// Bound by HBM: each raw row is read once and each result written once; the two special-function
+// calls per value (16 a cycle and SM) come next, at two thirds of that time in bf16.  One thread owns
+// VEC neighbouring channels (16 bytes) and a tile of consecutive rows: its taps and the three-row
+// window stay in registers, and the next kConvBatch rows are loaded while the present ones are
+// computed.  A tile is as long as one wave of CTAs allows, since a thread's 5 VEC taps and biases are
+// as many bytes as ten rows of bf16: 32-row tiles spent longer on them (161 us for 16384 x 6144)
+// than on the rows.  Only the window's three rows are read twice.
 #pragma once
 
 #include "ssm_common.cuh"
@@ -16,7 +18,7 @@ namespace gdn {
 namespace ssm {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvBatch = 8;       // rows whose loads are in flight together
+constexpr int kConvBatch = 4;       // rows loaded ahead
 
 // Rows [a, b) of sequence s, clamped like row_span; the same for dense and packed tensors.
 __device__ __forceinline__ void seq_rows(const int* __restrict__ cu, int s, int T, int max_len,
@@ -38,23 +40,24 @@ __device__ __forceinline__ int seq_of_row(const int* __restrict__ cu, int nseq, 
   return lo;
 }
 
+// VEC neighbouring channels of a row as loaded, and as pairs for the paired fp32 instructions (a single channel
+// leaves the second of its pair unused).
 template <typename T, int VEC> struct Piece;
 template <> struct Piece<__nv_bfloat16, 8> {
   uint4 v;
-  __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(f2_t (&f)[4]) const {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = pk2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
   }
-  static __device__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const f2_t (&f)[4]) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      float a, b;
+      up2(f[i], a, b);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
       u[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
@@ -62,17 +65,27 @@ template <> struct Piece<__nv_bfloat16, 8> {
 };
 template <> struct Piece<float, 4> {
   float4 v;
-  __device__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
-  __device__ void get(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
-  static __device__ void store(float* p, const float (&f)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(f2_t (&f)[2]) const {
+    f[0] = pk2(v.x, v.y);
+    f[1] = pk2(v.z, v.w);
+  }
+  static __device__ __forceinline__ void store(float* p, const f2_t (&f)[2]) {
+    float4 o;
+    up2(f[0], o.x, o.y);
+    up2(f[1], o.z, o.w);
+    *reinterpret_cast<float4*>(p) = o;
   }
 };
 template <typename T> struct Piece<T, 1> {   // any alignment
   T v;
-  __device__ void load(const T* p) { v = *p; }
-  __device__ void get(float (&f)[1]) const { f[0] = to_f(v); }
-  static __device__ void store(T* p, const float (&f)[1]) { *p = from_f<T>(f[0]); }
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void get(f2_t (&f)[1]) const { f[0] = pk2(to_f(v), 0.f); }
+  static __device__ __forceinline__ void store(T* p, const f2_t (&f)[1]) {
+    float a, b;
+    up2(f[0], a, b);
+    *p = from_f<T>(a);
+  }
 };
 
 struct ConvArgs {
@@ -83,15 +96,18 @@ struct ConvArgs {
   void *out, *hist_out; // [rows, C]; [nseq, 3, C] or null
   const int* cu;        // null: nseq sequences of T rows
   int nseq, T, max_len, C;
+  int tile;             // rows of a thread, a multiple of kConvBatch
+  int w_vec;            // w and bias allow 16-byte loads
 };
 
 // grid (row tiles + 1, channel blocks): the last row tile hands the history of sequences without
 // rows on.
-template <typename T, int VEC, int R>
+template <typename T, int VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a) {
   const int c = (blockIdx.y * kConvThreads + threadIdx.x) * VEC;
   if (c >= a.C) return;
   using Pc = Piece<T, VEC>;
+  constexpr int NP = (VEC + 1) / 2;
   const T* __restrict__ x = static_cast<const T*>(a.x) + c;
   const T* __restrict__ hin = a.hist_in ? static_cast<const T*>(a.hist_in) + c : nullptr;
   T* __restrict__ hout = a.hist_out ? static_cast<T*>(a.hist_out) + c : nullptr;
@@ -105,7 +121,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a) {
       seq_rows(a.cu, s, a.T, a.max_len, r0, r1);
       if (r1 > r0) continue;
       for (int i = 0; i < 3; ++i) {
-        float f[VEC] = {};
+        f2_t f[NP] = {};
         if (hin) {
           Pc p;
           p.load(hin + (3L * s + i) * C);
@@ -118,22 +134,39 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a) {
   }
 
   const long rows = a.cu ? (long)a.T : (long)a.nseq * a.T;
-  const long first = (long)blockIdx.x * R;
-  const long last = min(first + R, rows);
+  const long first = (long)blockIdx.x * a.tile;
+  const long last = min(first + a.tile, rows);
   int s = seq_of_row(a.cu, a.nseq, a.T, first);
   long r0, r1;
   seq_rows(a.cu, s, a.T, a.max_len, r0, r1);
 
-  float w[4][VEC], b[VEC];
+  f2_t w[4][NP], b[NP];
+  {
+    float ws[4][2 * NP] = {}, bs[2 * NP] = {};
+    if (VEC > 1 && a.w_vec) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    b[i] = a.bias ? a.bias[c + i] : 0.f;
+      for (int i = 0; i < VEC; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(a.w + 4L * (c + i));
+        ws[0][i] = v.x; ws[1][i] = v.y; ws[2][i] = v.z; ws[3][i] = v.w;
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j][i] = a.w[4L * (c + i) + j];
+      for (int i = 0; i < VEC; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ws[j][i] = a.w[4L * (c + i) + j];
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) bs[i] = a.bias ? a.bias[c + i] : 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      b[i] = pk2(bs[2 * i], bs[2 * i + 1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j][i] = pk2(ws[j][2 * i], ws[j][2 * i + 1]);
+    }
   }
   // window: the raw rows t-3, t-2, t-1
-  float w0[VEC], w1[VEC], w2[VEC];
-  auto prev = [&](long r, int back, float (&f)[VEC]) {   // the raw row `back` rows before row r
+  f2_t w0[NP], w1[NP], w2[NP];
+  auto prev = [&](long r, int back, f2_t (&f)[NP]) {   // the raw row `back` rows before row r
     const long t = r - back;
     Pc p;
     if (t >= r0) {
@@ -144,18 +177,26 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a) {
       p.get(f);
     } else {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) f[i] = 0.f;
+      for (int i = 0; i < NP; ++i) f[i] = 0;
     }
   };
   prev(first, 3, w0);
   prev(first, 2, w1);
   prev(first, 1, w2);
 
-  for (long base = first; base < last; base += kConvBatch) {
-    Pc rowv[kConvBatch];
+  Pc next[kConvBatch];
+  auto fetch = [&](long base) {
 #pragma unroll
     for (int i = 0; i < kConvBatch; ++i)
-      if (base + i < last) rowv[i].load(x + (base + i) * a.ldx);
+      if (base + i < last) next[i].load(x + (base + i) * a.ldx);
+  };
+  fetch(first);
+#pragma unroll 1
+  for (long base = first; base < last; base += kConvBatch) {
+    Pc now[kConvBatch];
+#pragma unroll
+    for (int i = 0; i < kConvBatch; ++i) now[i] = next[i];
+    fetch(base + kConvBatch);
 #pragma unroll
     for (int i = 0; i < kConvBatch; ++i) {
       const long r = base + i;
@@ -173,21 +214,23 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a) {
           prev(r, 2, w1);
           prev(r, 1, w2);
         }
-        float u[VEC], o[VEC];
-        rowv[i].get(u);
+        f2_t u[NP], o[NP];
+        now[i].get(u);
         if (r >= r0 && r < r1) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            float acc = fmaf(w[0][e], w0[e], b[e]);
-            acc = fmaf(w[1][e], w1[e], acc);
-            acc = fmaf(w[2][e], w2[e], acc);
-            acc = fmaf(w[3][e], u[e], acc);
-            o[e] = silu(acc);
+          for (int e = 0; e < NP; ++e) {
+            f2_t acc = fma2(w[0][e], w0[e], b[e]);
+            acc = fma2(w[1][e], w1[e], acc);
+            acc = fma2(w[2][e], w2[e], acc);
+            acc = fma2(w[3][e], u[e], acc);
+            float s0, s1;
+            up2(acc, s0, s1);
+            o[e] = mul2(acc, pk2(sigmoid(s0), VEC > 1 ? sigmoid(s1) : 0.f));
           }
           Pc::store(out + r * C, o);
         }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
+        for (int e = 0; e < NP; ++e) {
           w0[e] = w1[e];
           w1[e] = w2[e];
           w2[e] = u[e];
