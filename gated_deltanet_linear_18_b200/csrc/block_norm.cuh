@@ -195,31 +195,33 @@ __device__ __forceinline__ float group_sum(float v, float* red, int g, int t, in
   group_sync(g, nt);
   return warp_sum((t & 31) < (nt >> 5) ? red[t & 31] : 0.f);
 }
-// Four warp-wide sums in six shuffles: the halves, then the quarters of the warp each keep some of the values.  Lane
-// 8 i ends with the sum of v[i].
-__device__ __forceinline__ float warp_sum4(float4 v, int lane) {
-  const bool hi = lane & 16, odd = lane & 8;
-  const float a = (hi ? v.z : v.x) + __shfl_xor_sync(0xffffffffu, hi ? v.x : v.z, 16);
-  const float b = (hi ? v.w : v.y) + __shfl_xor_sync(0xffffffffu, hi ? v.y : v.w, 16);
-  float x = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-// Three sums over the group; one sync.  red: [32][4] floats.
-__device__ __forceinline__ void group_sum3(float& p, float& q, float& r, float* red, int g, int t, int nt) {
+// Six sums over the group; one sync.  In a warp, eight values (two of them zeros) take nine shuffles: with each of the
+// first three steps a lane gives half of its values away, so that lane 4 i ends with the sum of v[i].  Then each warp adds
+// the warps' parts, four lanes a value.  red: [warps][8] floats.
+__device__ __forceinline__ void group_sum6(float (&v)[6], float* red, int g, int t, int nt) {
   const int lane = t & 31;
-  float x = warp_sum4(make_float4(p, q, r, 0.f), lane);
+  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+  const float w[8] = {v[0], v[1], v[2], v[3], v[4], v[5], 0.f, 0.f};
+  float x4[4], x2[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x4[i] = (b4 ? w[i + 4] : w[i]) + __shfl_xor_sync(0xffffffffu, b4 ? w[i] : w[i + 4], 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x2[i] = (b3 ? x4[i + 2] : x4[i]) + __shfl_xor_sync(0xffffffffu, b3 ? x4[i] : x4[i + 2], 8);
+  float x = (b2 ? x2[1] : x2[0]) + __shfl_xor_sync(0xffffffffu, b2 ? x2[0] : x2[1], 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 2);
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
   if (nt == 32) {
     __syncwarp();
   } else {
-    if ((lane & 7) == 0) red[(t >> 5) * 4 + (lane >> 3)] = x;
+    if ((lane & 3) == 0) red[(t >> 5) * 8 + (lane >> 2)] = x;
     group_sync(g, nt);
-    x = warp_sum4(lane < (nt >> 5) ? reinterpret_cast<const float4*>(red)[lane] : make_float4(0.f, 0.f, 0.f, 0.f), lane);
+    x = 0.f;
+    for (int i = lane & 3; i < (nt >> 5); i += 4) x += red[i * 8 + (lane >> 2)];
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
   }
-  p = __shfl_sync(0xffffffffu, x, 0);
-  q = __shfl_sync(0xffffffffu, x, 8);
-  r = __shfl_sync(0xffffffffu, x, 16);
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, x, 4 * i);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -317,12 +319,14 @@ __global__ void __launch_bounds__(MAXT) fwd_kernel(const FwdArgs a, const Ring r
 // ---------------------------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------------------------
+// One sync a row: mean(w_post n' y), which needs dh, is linear in the row's scalars,
+//   sum w_post n' y = sum g h'' + r sum g w_pre x' - r (r^2 mean(w_pre x' h')) sum g h',  g = s SiLU(z) w_post y,
+// so all six sums are taken in one go before any output is formed.
 template <typename T, typename TH, int K, int MAXT>
 __global__ void __launch_bounds__(MAXT) bwd_kernel(const BwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[kMaxGroups][kMaxStages];
-  __shared__ __align__(16) float red3[kMaxGroups][128];
-  __shared__ float red1[kMaxGroups][32];
+  __shared__ float red[2][256];          // [warps][8], a group's at its first warp; rows alternate
   __shared__ int abort_word;
   Walk w;
   w.init(ring, smem, bars, &abort_word, a.w_post, a.scale, a.w_pre, a.D, a.rows);
@@ -336,14 +340,15 @@ __global__ void __launch_bounds__(MAXT) bwd_kernel(const BwdArgs a, const Ring r
 #pragma unroll
     for (int e = 0; e < 4; ++e) ga[k][e] = gn[k][e] = 0;
   const float invD = 1.0f / (float)a.D;
+  const f2_t one = splat2(1.f), minus = splat2(-1.f);
 #pragma unroll 1
   for (long i = 0; i < w.mine; ++i) {
     const long at = (w.row0 + i * w.step) * a.D;
     const unsigned char* base = w.wait(ring);
     Piece8<T> yv[K], zv[K], dx[K];
     Piece8<TH> hv[K], dh[K];
-    // the three sums that do not need dh: y^2, h'^2, w_pre x' h'
-    f2_t qy = 0, qh = 0, qx = 0;
+    f2_t sg[K][4];                       // sigmoid(z)
+    f2_t q[6] = {0, 0, 0, 0, 0, 0};      // y^2, h'^2, w_pre x' h', and the sums of g h'', g w_pre x', g h'
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * nt + t) * 8;
@@ -352,14 +357,35 @@ __global__ void __launch_bounds__(MAXT) bwd_kernel(const BwdArgs a, const Ring r
       dx[k].zero();
       hv[k].zero();
       dh[k].zero();
-      if (c < a.D) {
-        yv[k].load(reinterpret_cast<const T*>(base + ring.off[0]) + c);
-        if (a.z) zv[k].load(reinterpret_cast<const T*>(base + ring.off[2]) + c);
-        if (a.dh_in) dh[k].load(reinterpret_cast<const TH*>(base + ring.off[3]) + c);
-        f2_t f[4];
-        yv[k].get(f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) qy = fma2(f[e], f[e], qy);
+      for (int e = 0; e < 4; ++e) sg[k][e] = 0;
+      if (c < a.D) {
+        f2_t y[4], gv[4], f[4];
+        yv[k].load(reinterpret_cast<const T*>(base + ring.off[0]) + c);
+        yv[k].get(y);
+        ldv(sw + c, gv);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          q[0] = fma2(y[e], y[e], q[0]);
+          gv[e] = mul2(gv[e], y[e]);
+        }
+        if (a.z) {
+          zv[k].load(reinterpret_cast<const T*>(base + ring.off[2]) + c);
+          zv[k].get(f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float z0, z1;
+            up2(f[e], z0, z1);
+            sg[k][e] = pk2(sigm(z0), sigm(z1));
+            gv[e] = mul2(gv[e], mul2(f[e], sg[k][e]));
+          }
+        }
+        if (a.dh_in) {
+          dh[k].load(reinterpret_cast<const TH*>(base + ring.off[3]) + c);
+          dh[k].get(f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[3] = fma2(gv[e], f[e], q[3]);
+        }
         if (pre) {
           hv[k].load(reinterpret_cast<const TH*>(base + ring.off[1]) + c);
           dx[k].load(reinterpret_cast<const T*>(base + ring.off[4]) + c);
@@ -369,26 +395,29 @@ __global__ void __launch_bounds__(MAXT) bwd_kernel(const BwdArgs a, const Ring r
           ldv(wn + c, u);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            qh = fma2(f[e], f[e], qh);
-            qx = fma2(mul2(f[e], u[e]), d[e], qx);
+            const f2_t wx = mul2(u[e], d[e]);
+            q[1] = fma2(f[e], f[e], q[1]);
+            q[2] = fma2(wx, f[e], q[2]);
+            q[4] = fma2(gv[e], wx, q[4]);
+            q[5] = fma2(gv[e], f[e], q[5]);
           }
         }
       }
     }
-    float sy = hsum2(qy), sh = hsum2(qh), sx = hsum2(qx);
-    group_sum3(sy, sh, sx, red3[g], g, t, nt);
+    float s[6];
+#pragma unroll
+    for (int e = 0; e < 6; ++e) s[e] = hsum2(q[e]);
+    group_sum6(s, red[i & 1] + g * (nt >> 5) * 8, g, t, nt);
     w.refill(ring, i);
-    const float ry = post ? rsqrtf(fmaf(sy, invD, a.eps)) : 1.f;
-    const float rh = pre ? rsqrtf(fmaf(sh, invD, a.eps)) : 0.f;
-    const f2_t ry2 = splat2(ry), rh2 = splat2(rh), mx2 = splat2(-rh * rh * sx * invD);
-    const f2_t one = splat2(1.f), minus = splat2(-1.f);
-    f2_t u[K][4];                        // n' w_post: what dy starts from
-    f2_t qd = 0;                         // w_post n' y
+    const float ry = post ? rsqrtf(fmaf(s[0], invD, a.eps)) : 1.f;
+    const float rh = pre ? rsqrtf(fmaf(s[1], invD, a.eps)) : 0.f;
+    const float mx = rh * rh * s[2] * invD;
+    const float qd = fmaf(rh, fmaf(-mx, s[5], s[4]), s[3]);
+    const f2_t ry2 = splat2(ry), rh2 = splat2(rh), mx2 = splat2(-mx);
+    const f2_t my2 = splat2(post ? -ry * ry * ry * qd * invD : 0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * nt + t) * 8;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[k][e] = 0;
       if (c < a.D) {
         f2_t d[4], y[4], f[4], v[4];
         dh[k].get(d);
@@ -410,43 +439,21 @@ __global__ void __launch_bounds__(MAXT) bwd_kernel(const BwdArgs a, const Ring r
           zv[k].get(z);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float z0, z1;
-            up2(z[e], z0, z1);
-            const f2_t s = pk2(sigm(z0), sigm(z1)), gate = mul2(z[e], s);
-            const f2_t yr = mul2(y[e], ry2), as = mul2(d[e], v[e]);
-            f[e] = mul2(mul2(as, yr), mul2(s, fma2(z[e], fma2(s, minus, one), one)));
+            const f2_t gate = mul2(z[e], sg[k][e]), yr = mul2(y[e], ry2), as = mul2(d[e], v[e]);
+            f[e] = mul2(mul2(as, yr), mul2(sg[k][e], fma2(z[e], fma2(sg[k][e], minus, one), one)));
             ga[k][e] = fma2(mul2(d[e], gate), yr, ga[k][e]);
-            u[k][e] = mul2(as, gate);
-            qd = fma2(u[k][e], y[e], qd);
+            d[e] = fma2(y[e], my2, mul2(mul2(as, gate), ry2));
           }
           Piece8<T>::store(static_cast<T*>(a.dz) + at + c, f);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             ga[k][e] = fma2(d[e], mul2(y[e], ry2), ga[k][e]);
-            u[k][e] = mul2(d[e], v[e]);
-            qd = fma2(u[k][e], y[e], qd);
+            d[e] = fma2(y[e], my2, mul2(mul2(d[e], v[e]), ry2));
           }
         }
+        Piece8<T>::store(static_cast<T*>(a.dy) + at + c, d);
       }
-    }
-    if (post) {
-      const float my = ry * ry * group_sum(hsum2(qd), red1[g], g, t, nt) * invD;
-      const f2_t my2 = splat2(-ry * my);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        f2_t y[4];
-        yv[k].get(y);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[k][e] = fma2(y[e], my2, mul2(u[k][e], ry2));
-      }
-    } else {
-      group_sync(g, nt);                 // red3 is written again in the next row
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * nt + t) * 8;
-      if (c < a.D) Piece8<T>::store(static_cast<T*>(a.dy) + at + c, u[k]);
     }
   }
   float* part = a.part + ((long)blockIdx.x * ring.groups + g) * 2 * a.D;
