@@ -703,25 +703,33 @@ def check_error(device: Optional[torch.device] = None):
 # ------------------------------------------------------------------------------------------------
 # selective state space block
 # ------------------------------------------------------------------------------------------------
-def _cuda(*ts: Optional[torch.Tensor]) -> torch.device:
-    """The one CUDA device of the tensors (any layout)."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("all tensors must be on one device")
+# These calls also serve single tokens, where the host's time is the call's: their checks look at sizes
+# and strides as plain tuples and at devices as plain numbers.
+def _on(*ts: Optional[torch.Tensor]) -> int:
+    """The one CUDA device (its number) of the tensors, any layout."""
+    devs = {t.get_device() for t in ts if t is not None}
+    dev = devs.pop()
+    if dev < 0 or -1 in devs:
+        raise ValueError("all tensors must be CUDA tensors")
+    if devs:
+        raise ValueError("all tensors must be on one device")
     return dev
 
 
 def _dense(*ts: Optional[torch.Tensor]):
     for t in ts:
         if t is not None and not t.is_contiguous():
-            raise ValueError("states, histories, weights and offsets must be contiguous")
+            raise ValueError("states, histories, weights, offsets, outputs and norm inputs must be contiguous")
+
+
+def _fp32(*ts: Optional[torch.Tensor]):
+    for t in ts:
+        if t is not None and t.dtype is not torch.float32:
+            raise ValueError("gates, states and weights must be float32")
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _row_ld(t: Optional[torch.Tensor], lead: int, name: str) -> int:
@@ -730,37 +738,46 @@ def _row_ld(t: Optional[torch.Tensor], lead: int, name: str) -> int:
     a contiguous tensor, or a contiguous tensor."""
     if t is None:
         return 0
+    stride = t.stride()
+    if lead == 1 and len(stride) == 2 and stride[1] == 1 and stride[0] >= t.shape[1]:
+        return stride[0]
+    shape = t.shape
     want = 1
-    for i in range(t.dim() - 1, lead - 1, -1):
-        if t.shape[i] > 1 and t.stride(i) != want:
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if stride[i] != want and shape[i] > 1:
             raise ValueError(f"{name}: the values of a token must be contiguous")
-        want *= t.shape[i]
-    ld, span = max(want, 1), None
-    for i in range(lead - 1, -1, -1):
-        if t.shape[i] > 1:
-            if span is None:
-                ld = span = t.stride(i)
-            elif t.stride(i) != span:
-                raise ValueError(f"{name}: the tokens must be evenly spaced")
-        if span is not None:
-            span *= t.shape[i]
+        want *= shape[i]
+    if lead == 1:
+        ld = stride[0] if shape[0] > 1 else max(want, 1)
+    else:
+        ld, span = max(want, 1), None
+        for i in range(lead - 1, -1, -1):
+            if shape[i] > 1:
+                if span is None:
+                    ld = span = stride[i]
+                elif stride[i] != span:
+                    raise ValueError(f"{name}: the tokens must be evenly spaced")
+            if span is not None:
+                span *= shape[i]
     if ld < want:
         raise ValueError(f"{name}: the tokens overlap")
     return ld
 
 
-def _call(name: str, dev: torch.device, *args):
-    """Call the library on ``dev``'s current stream (made current where it is not)."""
-    fn = getattr(lib(), name)
-    stream = _stream(dev)
-    if torch.cuda.current_device() == dev.index:
-        _check(name, fn(*args, stream))
+def _call(name: str, dev: int, *args):
+    """Call the library on the current stream of device ``dev`` (made current where it is not)."""
+    fn = getattr(_lib or lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(name, fn(*args, stream))
+            status = fn(*args, stream)
+    if status:
+        raise GdnError(name, status)
 
 
-def _conv(x, lead, w, bias, hist, nseq, want_hist, out):
+def _conv(x, lead, w, bias, hist, nseq, want_hist, out, cu=None):
     C = x.shape[-1]
     if w.shape != (C, 4) or (bias is not None and bias.shape != (C,)):
         raise ValueError("w must be [C, 4] and bias [C]")
@@ -768,14 +785,15 @@ def _conv(x, lead, w, bias, hist, nseq, want_hist, out):
         raise ValueError("hist must be [sequences, 3, C] in x's dtype")
     if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
         raise ValueError("out must have x's shape and dtype")
-    _f32(w, bias)
+    _fp32(w, bias)
     io = _io_dtype(x)
     _dense(w, bias, hist, out)
     ld = _row_ld(x, lead, "x")
+    dev = _on(x, w, bias, hist, out, cu)
     if out is None:
-        out = torch.empty(x.shape, device=x.device, dtype=x.dtype)
-    hist_out = torch.empty(nseq, 3, C, device=x.device, dtype=x.dtype) if want_hist else None
-    return out, hist_out, ld, io, _cuda(x, w, bias, hist, out)
+        out = x.new_empty(x.shape)
+    hist_out = x.new_empty((nseq, 3, C)) if want_hist else None
+    return out, hist_out, ld, io, dev
 
 
 def ssm_conv(x, w, bias=None, *, hist=None, want_hist: bool = False,
@@ -787,9 +805,16 @@ def ssm_conv(x, w, bias=None, *, hist=None, want_hist: bool = False,
         raise ValueError("x must be [B, T, C]")
     B, T, C = x.shape
     out, hist_out, ld, io, dev = _conv(x, 2, w, bias, hist, B, want_hist, out)
-    _call("gdn_ssm_conv", dev, _p(x), ld, _p(w), _p(bias), _p(hist), _p(out), _p(hist_out), B, T, C,
-          io)
+    _call("gdn_ssm_conv", dev, x.data_ptr(), ld, w.data_ptr(), _ptr(bias), _ptr(hist), out.data_ptr(),
+          _ptr(hist_out), B, T, C, io)
     return (out, hist_out) if want_hist else out
+
+
+def _offsets(cu_seqlens) -> int:
+    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 \
+            or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32 [nseq + 1]")
+    return cu_seqlens.shape[0] - 1
 
 
 def ssm_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, *, hist=None, want_hist: bool = False,
@@ -798,13 +823,10 @@ def ssm_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, *, hist=None, want_
     [nseq,3,C].  Rows in no sequence keep their ``out``."""
     if x.dim() != 2:
         raise ValueError("x must be [total, C]")
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be contiguous int32 [nseq + 1]")
-    nseq = cu_seqlens.numel() - 1
-    out, hist_out, ld, io, dev = _conv(x, 1, w, bias, hist, nseq, want_hist, out)
-    _cuda(x, cu_seqlens)
-    _call("gdn_ssm_conv_varlen", dev, _p(x), ld, _p(w), _p(bias), _p(cu_seqlens), nseq,
-          int(max_seqlen), _p(hist), _p(out), _p(hist_out), x.shape[0], x.shape[1], io)
+    nseq = _offsets(cu_seqlens)
+    out, hist_out, ld, io, dev = _conv(x, 1, w, bias, hist, nseq, want_hist, out, cu_seqlens)
+    _call("gdn_ssm_conv_varlen", dev, x.data_ptr(), ld, w.data_ptr(), _ptr(bias), cu_seqlens.data_ptr(), nseq,
+          int(max_seqlen), _ptr(hist), out.data_ptr(), _ptr(hist_out), x.shape[0], x.shape[1], io)
     return (out, hist_out) if want_hist else out
 
 
@@ -814,38 +836,41 @@ def ssm_scan_workspace_bytes(nseq, max_seqlen, H, G, P, N, dtype) -> int:
 
 
 def _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, lead, nseq, max_len, want_state, out, state_out,
-          workspace):
-    H, P = x.shape[lead:]
-    tok = tuple(x.shape[:lead])
-    if dt.shape != tok + (H,) or Bm.dim() != lead + 2 or tuple(Bm.shape[:lead]) != tok \
-            or Cm.shape != Bm.shape or (z is not None and z.shape != x.shape):
+          workspace, cu=None):
+    shape = tuple(x.shape)
+    H, P = shape[lead:]
+    tok = shape[:lead]
+    bs = tuple(Bm.shape)
+    if dt.shape != tok + (H,) or len(bs) != lead + 2 or bs[:lead] != tok or Cm.shape != bs \
+            or (z is not None and z.shape != shape):
         raise ValueError("x, dt, Bm, Cm, z shapes disagree")
-    G, N = Bm.shape[lead:]
-    for t in (dt, Bm, Cm, z):
-        if t is not None and t.dtype != x.dtype:
-            raise ValueError("x, dt, Bm, Cm, z must have one dtype")
+    G, N = bs[lead:]
+    ty = x.dtype
+    if dt.dtype != ty or Bm.dtype != ty or Cm.dtype != ty or (z is not None and z.dtype != ty):
+        raise ValueError("x, dt, Bm, Cm, z must have one dtype")
     for t in (A_log, D, dt_bias):
         if t is not None and t.shape != (H,):
             raise ValueError("A_log, D, dt_bias must be [H]")
     for t in (S0, state_out):
         if t is not None and t.shape != (nseq, H, N, P):
             raise ValueError("states must be [sequences, H, N, P]")
-    if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
+    if out is not None and (out.shape != shape or out.dtype != ty):
         raise ValueError("out must have x's shape and dtype")
-    _f32(A_log, D, dt_bias, S0, state_out)
+    _fp32(A_log, D, dt_bias, S0, state_out)
     io = _io_dtype(x)
     _dense(A_log, D, dt_bias, S0, state_out, out, workspace)
-    y = torch.empty(x.shape, device=x.device, dtype=x.dtype) if out is None else out
+    dev = _on(x, dt, Bm, Cm, z, A_log, D, dt_bias, S0, out, state_out, workspace, cu)
+    lds = (_row_ld(x, lead, "x"), _row_ld(dt, lead, "dt"), _row_ld(Bm, lead, "Bm"), _row_ld(Cm, lead, "Cm"),
+           _row_ld(z, lead, "z"))
+    y = x.new_empty(shape) if out is None else out
     sT = state_out
     if sT is None and want_state:
-        sT = torch.empty(nseq, H, N, P, device=x.device, dtype=torch.float32)
-    dev = _cuda(x, dt, Bm, Cm, z, A_log, D, dt_bias, S0, y, sT, workspace)
-    need = int(lib().gdn_ssm_scan_workspace_bytes(nseq, max_len, H, G, P, N, io))
-    ws, wbytes = _workspace(need, dev, workspace)
-    head = (_p(x), _row_ld(x, lead, "x"), _p(dt), _row_ld(dt, lead, "dt"), _p(Bm),
-            _row_ld(Bm, lead, "Bm"), _p(Cm), _row_ld(Cm, lead, "Cm"), _p(z), _row_ld(z, lead, "z"),
-            _p(A_log), _p(D), _p(dt_bias))
-    return y, sT, head, (_p(S0), _p(y), _p(sT), _p(ws), wbytes), (H, G, P, N, io), dev
+        sT = A_log.new_empty((nseq, H, N, P))
+    need = (_lib or lib()).gdn_ssm_scan_workspace_bytes(nseq, max_len, H, G, P, N, io)
+    ws, wbytes = _workspace(need, x.device, workspace)
+    head = (x.data_ptr(), lds[0], dt.data_ptr(), lds[1], Bm.data_ptr(), lds[2], Cm.data_ptr(), lds[3], _ptr(z),
+            lds[4], A_log.data_ptr(), _ptr(D), _ptr(dt_bias))
+    return y, sT, ws, head, (_ptr(S0), y.data_ptr(), _ptr(sT), _ptr(ws), wbytes), (H, G, P, N, io), dev
 
 
 def ssm_scan(x, dt, A_log, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None,
@@ -859,8 +884,8 @@ def ssm_scan(x, dt, A_log, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None,
     if x.dim() != 4:
         raise ValueError("x must be [B, T, H, P]")
     B, T = x.shape[:2]
-    y, sT, head, mid, dims, dev = _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, 2, B, T, want_state,
-                                        out, state_out, workspace)
+    y, sT, ws, head, mid, dims, dev = _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, 2, B, T, want_state,
+                                            out, state_out, workspace)
     _call("gdn_ssm_scan", dev, *head, *mid, B, T, *dims)
     return y, sT
 
@@ -875,13 +900,10 @@ def ssm_scan_varlen(x, dt, A_log, Bm, Cm, cu_seqlens, max_seqlen: int, *, D=None
     (device), states [nseq,H,N,P].  Rows in no sequence keep their ``out``."""
     if x.dim() != 3:
         raise ValueError("x must be [total, H, P]")
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be contiguous int32 [nseq + 1]")
-    nseq, max_seqlen = cu_seqlens.numel() - 1, int(max_seqlen)
-    y, sT, head, mid, dims, dev = _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, 1, nseq, max_seqlen,
-                                        want_state, out, state_out, workspace)
-    _cuda(x, cu_seqlens)
-    _call("gdn_ssm_scan_varlen", dev, *head, _p(cu_seqlens), nseq, max_seqlen, *mid, x.shape[0], *dims)
+    nseq, max_seqlen = _offsets(cu_seqlens), int(max_seqlen)
+    y, sT, ws, head, mid, dims, dev = _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, 1, nseq, max_seqlen,
+                                            want_state, out, state_out, workspace, cu_seqlens)
+    _call("gdn_ssm_scan_varlen", dev, *head, cu_seqlens.data_ptr(), nseq, max_seqlen, *mid, x.shape[0], *dims)
     return y, sT
 
 
@@ -902,35 +924,42 @@ def ssm_step(u, dt, hist, w, bias, A_log, S, *, groups: int, D=None, z=None, dt_
     for t in (A_log, D, dt_bias):
         if t is not None and t.shape != (H,):
             raise ValueError("A_log, D, dt_bias must be [H]")
-    hist_out = torch.empty(hist.shape, device=hist.device, dtype=hist.dtype) if hist_out is None else hist_out
-    y = torch.empty(n, H, P, device=u.device, dtype=u.dtype) if out is None else out
-    if hist_out.shape != hist.shape or y.shape != (n, H, P):
-        raise ValueError("hist_out or out has another shape")
-    for t in (dt, hist, hist_out, z, y):
-        if t is not None and t.dtype != u.dtype:
-            raise ValueError("u, dt, hist, z and the outputs must have one dtype")
-    _f32(w, bias, A_log, D, dt_bias, S)
-    _dense(hist, hist_out, w, bias, A_log, D, dt_bias, S, y)
-    dev = _cuda(u, dt, hist, w, bias, A_log, S, D, z, dt_bias, hist_out, y)
-    _call("gdn_ssm_step", dev, _p(u), _row_ld(u, 1, "u"), _p(dt), _row_ld(dt, 1, "dt"), _p(z),
-          _row_ld(z, 1, "z"), _p(hist), _p(hist_out), _p(w), _p(bias), _p(A_log), _p(D), _p(dt_bias),
-          _p(S), _p(y), n, H, groups, P, N, _io_dtype(u))
-    return y, hist_out
+    ty = u.dtype
+    if hist_out is None:
+        hist_out = hist.new_empty((n, 3, C))
+    elif hist_out.shape != (n, 3, C):
+        raise ValueError("hist_out has another shape")
+    if out is None:
+        out = u.new_empty((n, H, P))
+    elif out.shape != (n, H, P):
+        raise ValueError("out has another shape")
+    if dt.dtype != ty or hist.dtype != ty or hist_out.dtype != ty or out.dtype != ty \
+            or (z is not None and z.dtype != ty):
+        raise ValueError("u, dt, hist, z and the outputs must have one dtype")
+    _fp32(w, bias, A_log, D, dt_bias, S)
+    _dense(hist, hist_out, w, bias, A_log, D, dt_bias, S, out)
+    dev = _on(u, dt, hist, w, bias, A_log, S, D, z, dt_bias, hist_out, out)
+    _call("gdn_ssm_step", dev, u.data_ptr(), _row_ld(u, 1, "u"), dt.data_ptr(), _row_ld(dt, 1, "dt"), _ptr(z),
+          _row_ld(z, 1, "z"), hist.data_ptr(), hist_out.data_ptr(), w.data_ptr(), _ptr(bias), A_log.data_ptr(),
+          _ptr(D), _ptr(dt_bias), S.data_ptr(), out.data_ptr(), n, H, groups, P, N, _io_dtype(u))
+    return out, hist_out
 
 
 # ------------------------------------------------------------------------------------------------
 # the norms before and after a block
 # ------------------------------------------------------------------------------------------------
 def _norm_args(y, h, z, w_post, w_pre, res_scale):
-    D = y.shape[-1]
-    if h.shape != y.shape or (z is not None and z.shape != y.shape):
+    shape = y.shape
+    D = shape[-1]
+    if h.shape != shape or (z is not None and z.shape != shape):
         raise ValueError("y, h and z must have one shape")
     if z is not None and z.dtype != y.dtype:
         raise ValueError("y and z must have one dtype")
     for t in (w_post, w_pre, res_scale):
         if t is not None and t.shape != (D,):
             raise ValueError("w_post, w_pre and res_scale must be [D]")
-    _f32(w_post, w_pre, res_scale)
+    _fp32(w_post, w_pre, res_scale)
+    _dense(y, h, z, w_post, w_pre, res_scale)
     return (y.numel() // D if D else 0), D, _io_dtype(y), _io_dtype(h)
 
 
@@ -941,11 +970,11 @@ def block_norm(y, h, *, w_post=None, w_pre=None, z=None, res_scale=None, eps: fl
     or in float32; w_post, w_pre, res_scale [D] fp32, each optional.  Returns (h_out, x), x None
     without ``w_pre``."""
     rows, D, io, ho = _norm_args(y, h, z, w_post, w_pre, res_scale)
-    dev = _dev(y, h, z, w_post, w_pre, res_scale)
-    h_out = torch.empty(h.shape, device=dev, dtype=h.dtype)
-    x = None if w_pre is None else torch.empty(y.shape, device=dev, dtype=y.dtype)
-    _call("gdn_block_norm", dev, _p(y), _p(h), _p(z), _p(w_post), _p(w_pre), _p(res_scale), _p(h_out),
-          _p(x), rows, D, float(eps), io, ho)
+    dev = _on(y, h, z, w_post, w_pre, res_scale)
+    h_out = torch.empty_like(h)
+    x = None if w_pre is None else torch.empty_like(y)
+    _call("gdn_block_norm", dev, y.data_ptr(), h.data_ptr(), _ptr(z), _ptr(w_post), _ptr(w_pre), _ptr(res_scale),
+          h_out.data_ptr(), _ptr(x), rows, D, eps, io, ho)
     return h_out, x
 
 
@@ -966,12 +995,13 @@ def block_norm_bwd(y, h_out, dh_out, dx=None, *, w_post=None, w_pre=None, z=None
         raise ValueError("dh_out is needed without w_pre")
     if dh_out is not None and (dh_out.shape != y.shape or dh_out.dtype != h_out.dtype):
         raise ValueError("dh_out must have h_out's shape and dtype")
-    dev = _dev(y, h_out, dh_out, dx, z, w_post, w_pre, res_scale, workspace)
-    like = lambda t: None if t is None else torch.empty(t.shape, device=dev, dtype=t.dtype)
+    _dense(dh_out, dx, workspace)
+    dev = _on(y, h_out, dh_out, dx, z, w_post, w_pre, res_scale, workspace)
+    like = lambda t: None if t is None else torch.empty_like(t)
     g = {"dy": like(y), "dh": like(h_out), "dz": like(z), "dw_post": like(w_post), "dw_pre": like(w_pre),
          "dres_scale": like(res_scale)}
-    ws, wbytes = _workspace(block_norm_bwd_workspace_bytes(rows, D), dev, workspace)
-    _call("gdn_block_norm_bwd", dev, _p(y), _p(h_out), _p(z), _p(dh_out), _p(dx), _p(w_post), _p(w_pre),
-          _p(res_scale), _p(g["dy"]), _p(g["dh"]), _p(g["dz"]), _p(g["dw_post"]), _p(g["dw_pre"]),
-          _p(g["dres_scale"]), _p(ws), wbytes, rows, D, float(eps), io, ho)
+    ws, wbytes = _workspace((_lib or lib()).gdn_block_norm_bwd_workspace_bytes(rows, D), y.device, workspace)
+    _call("gdn_block_norm_bwd", dev, y.data_ptr(), h_out.data_ptr(), _ptr(z), _ptr(dh_out), _ptr(dx), _ptr(w_post),
+          _ptr(w_pre), _ptr(res_scale), g["dy"].data_ptr(), g["dh"].data_ptr(), _ptr(g["dz"]), _ptr(g["dw_post"]),
+          _ptr(g["dw_pre"]), _ptr(g["dres_scale"]), _ptr(ws), wbytes, rows, D, eps, io, ho)
     return g
