@@ -98,7 +98,7 @@ gdn_status check_heads(int H, int G, int P, int N) {
 
 size_t scan_workspace(int nseq, int max_len, int H, int G, int P, int N, gdn_dtype dtype) {
   if (dtype != GDN_BF16 || !ssm::tcs::supported(P, N)) return 0;
-  return ssm::tcs::workspace(nseq, max_len, H, G, P, N);
+  return ssm::tcs::space(nseq, max_len, H, G, P, N).bytes;
 }
 
 gdn_status scan_call(ssm::ScanArgs a, int P, int N, void* workspace, size_t workspace_bytes, gdn_dtype dtype,
@@ -126,9 +126,10 @@ gdn_status scan_call(ssm::ScanArgs a, int P, int N, void* workspace, size_t work
   if (need && rows > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return GDN_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const void* tiles[] = {a.x, a.B, a.C};
+  const void* tiles[] = {a.x, a.B, a.C, a.z};
   bool tc = dtype == GDN_BF16 && ssm::tcs::supported(P, N) && rows > 0 && rows <= 0x7fffffffL - 2 * ssm::tcs::L &&
-            a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0;
+            a.max_len > 0 && a.max_len <= 65535 * ssm::tcs::L && a.ldx % 8 == 0 && a.ldb % 8 == 0 && a.ldc % 8 == 0 &&
+            (!a.z || a.ldz % 8 == 0);
   for (const void* p : tiles) tc = tc && aligned(p, 16);
   if (tc) {
     if (P == 64) return (gdn_status)(N == 64 ? ssm::tcs::launch_np<64, 64>(a, workspace, st)

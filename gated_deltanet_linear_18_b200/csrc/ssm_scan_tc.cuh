@@ -21,14 +21,18 @@
 // that matter, keep their relative accuracy.  Across blocks P's factor is a product of a row's and a
 // column's exponential (both at most 1), so only the diagonal 32 x 32 blocks need one exponential each.
 //
-// Roles: four warpgroups that run ahead of one another as far as the tiles and accumulators allow.
-//   warp 0 loads B and C, warp 2 loads x tiles and stores y, warp 1 issues the MMAs in the order
-//     U (first 64 tokens), G, U (last 64), Yi, Ya of each chunk;
-//   warpgroup 1 forms the decays and X' of the next chunk while this one is multiplied (it reads x from
-//     global memory into registers, so that the x tile can hold y until that is stored);
+// Roles: five warpgroups that run ahead of one another as far as the tiles and accumulators allow.
+//   warp 0 loads B, C and the chunks' decay vectors, warp 2 loads x tiles and stores y, warp 3 issues the MMAs of U in
+//     four quarters of 32 tokens, warp 1 those of G, Yi and Ya;
+//   warpgroup 1 forms X' (it reads x from global memory into registers, so that the x tile can hold y until
+//     that is stored);
 //   warpgroup 2 forms P and keeps the state in registers (a thread a row hp of S^T);
-//   warpgroup 3 forms y, in place of x in its tile, which leaves by a TMA store.
+//   warpgroups 3 and 4 form y, 64 columns each, in place of x in its tile, which leaves by a TMA store.
 // B and C, which the heads of a group share, come from L2.
+//
+// The decay vectors (five numbers a token and head) come from a small kernel before: formed here they were a role
+// of 1000 instructions run by one warp, and what bounds this kernel is how fast the SM gets its instructions
+// (78 KB of code for all roles; every role that got shorter made the others faster).
 //
 // A sequence may be cut into segments that run side by side: a first launch (kOut = false) leaves
 // each segment's own final state and its total decay in the workspace, and the second starts every
@@ -46,8 +50,8 @@ namespace ssm {
 namespace tcs {
 
 constexpr int L = 128;                        // tokens of a chunk
-constexpr int kThreads = 512;
-constexpr uint64_t kBudget = 4000000000ull;   // wait budget in SM cycles (about 2 s)
+constexpr int kThreads = 640;
+constexpr uint32_t kPolls = 1u << 24;         // polls of a barrier before a wait gives up (half a second or more)
 constexpr uint32_t kTile = L * 128;           // bytes of a [128 rows, 64 bf16] tile
 using bf16_t = __nv_bfloat16;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -55,37 +59,42 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Args {
   ScanArgs a;
   float* ws;                    // segment states, then segment decays (segments > 1)
+  const float* vecs;            // decay vectors: [nseq, columns, chunks] records of kVec bytes
+  int chunks;                   // chunks of the longest sequence
   int seg_chunks, segments;     // chunks of a segment; segments of the longest sequence
-  int z_vec;                    // z's rows allow 16-byte loads
 };
 
-// Vectors of a chunk (a ring of three): u, w, e, prefix, prefix - log2 step [2 heads][128];
-// block sums [2][4]; decay [2].
+constexpr uint32_t kSlot = 6 * kTile / 4;      // X' of 32 tokens: three terms, two 64-column quarter tiles each
+// The decay vectors of a chunk of two heads (exponents in base 2): u [2][128] D_s exp(suffix in its block), w [2][128]
+// D_s exp(suffix in the chunk), e [2][128] exp(prefix in the chunk), prefix in its block [2][128], the same less
+// log2 D_s [2][128], block sums [2][4], exp(chunk's sum) [2].
 constexpr uint32_t kVec = (2 * 128 * 5 + 16) * 4;
+constexpr int VU = 0, VW = 256, VE = 512, VP = 768, VT = 1280, VD = 1288;
 
-// Shared memory.  With the outputs: x tiles of two chunks, B, C, the state operand, X' of 64 tokens, vectors,
-// barriers.  Without: B of two chunks, X' of 128 tokens.
+// Shared memory.  With the outputs: x tiles of two chunks, B, C, the state operand, two slots of X' (32 tokens
+// each), vectors, barriers.  Without: B of two chunks.
 template <int N, bool kOut> struct Layout {
   static constexpr uint32_t NB = N / 64;
   static constexpr uint32_t x = 0;                                  // [2][2] tiles
   static constexpr uint32_t b = kOut ? 4 * kTile : 0;               // [1 or 2][NB] tiles
   static constexpr uint32_t c = b + (kOut ? 1 : 2) * NB * kTile;
   static constexpr uint32_t s = c + (kOut ? NB * kTile : 0);
-  static constexpr uint32_t xw = s + (kOut ? NB * kTile : 0);       // [1 or 2][3 terms][2] half tiles
-  static constexpr uint32_t xw_stage = 6 * kTile / 2;
-  static constexpr uint32_t vec = xw + (kOut ? 1 : 2) * xw_stage;
+  static constexpr uint32_t xw = s + (kOut ? NB * kTile : 0);       // [2 slots][3 terms][2] quarter tiles
+  static constexpr uint32_t vec = xw + 2 * kSlot;
   static constexpr uint32_t bars = vec + 3 * kVec;
   static constexpr uint32_t bytes = bars + 256;
   static constexpr uint32_t alloc = bytes + 1024;                   // the base is rounded up to 1024
   static_assert(alloc <= 232448, "shared memory of a CTA");
 };
 
-// Barriers.  By TMA: XF (two x tiles), BF (two B buffers), CF.  By MMA commits: U0, U1 (U's halves), BE (two B buffers
-// free again), GD (G), YI, YA.  By the 128 threads of a warpgroup: XT0, XT1 (X' halves and the chunk's vectors), PR
-// (P), UR (U is in registers), SR (the state operand), YR (y in its tile, Yi and Ya read).
+// Barriers.  By TMA: XF (two x tiles), BF (two B buffers), CF, VR (three vector slots).  By MMA commits: UQ (the two X' slots read), U1 (U
+// complete), BE (two B buffers free again), GD (G), YI, YA.  By the
+// threads of the warpgroups: XT (two X' slots staged), PR (P), UR (U is in registers), SR (the state operand), YR (y in
+// its tile, Yi and Ya read).
 // A wait names a phase by its parity alone, so each one below stands where the phase after the awaited
 // one cannot have completed: what completes that needs something this waiter has yet to do.  For the same
-// reason nobody but the MMA thread waits for XT0 / XT1; G, U and Y being complete implies the vectors.
+// reason only warp 3 waits for XT and only warpgroup 1 for VR; G, U and Y being complete implies the
+// vectors for the others.
 // log2 of a time step (0 gives -infinity: that token's weight is 0)
 __device__ __forceinline__ float log2_step(float v) {
   float r;
@@ -93,7 +102,28 @@ __device__ __forceinline__ float log2_step(float v) {
   return r;
 }
 
-enum Bar { XF = 0, BF = 2, CF = 4, U0, U1, BE, GD = BE + 2, YI, YA, XT0, XT1, PR, UR, SR, YR, DRAIN, kBars };
+enum Bar { XF = 0, BF = 2, CF = 4, UQ, U1 = UQ + 2, BE, GD = BE + 2, YI, YA, VR, DRAIN = VR + 3, XT, PR = XT + 2, UR, SR, YR, kBars };
+
+// Bounded wait in few instructions (there are many of them, and the roles' code has to stay in the instruction
+// cache): gives up after kPolls polls, or as soon as another thread has; the caller goes on with what is there and
+// the kernel reports it at its end.
+__device__ __forceinline__ void bounded_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+  for (uint32_t n = 0; !tc::mbar_try_wait(bar, parity); ++n)
+    if (n == kPolls || *abort_flag) {
+      *abort_flag = 1;
+      break;
+    }
+}
+
+// Rows `valid` .. 127 of `tiles` tiles to zeros, by 128 threads.
+__device__ __forceinline__ void zero_rows(uint32_t tile0, int tiles, int valid, int t) {
+#pragma unroll 1
+  for (int i = t; i < (L - valid) * 8 * tiles; i += 128) {
+    const int j = i & 7, tl = (i >> 3) % tiles, r = valid + (i >> 3) / tiles;
+    tc::st_shared_v4(tile0 + tl * kTile + tc::sw128(r, j), 0, 0, 0, 0);
+  }
+}
 
 template <int kRegs> __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -115,14 +145,42 @@ __device__ __forceinline__ void tma_store_2d(const void* map, uint32_t src, int 
                "r"(src), "r"(c0), "r"(c1)
                : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem desc]: lane = row of A, two bf16 of K per 32-bit column.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// The MMAs, run by a whole warp and issued by its `leader` lane: the descriptors then stay in uniform registers, where
+// an MMA issued from a branch of one thread moves each of them there first.  D[tmem] (+)= A * B; A from shared memory, or
+// from tmem (lane = row, two bf16 of K per 32-bit column).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
-      : "memory");
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -132,7 +190,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
@@ -143,6 +200,55 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The decay vectors of every chunk: grid (columns, chunks, sequences), 128 threads for each of the column's heads, a
+// token a thread and a block of 32 tokens a warp.
+template <int NH>
+__global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float* __restrict__ vecs) {
+  const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH;
+  const int g = blockIdx.x / pairs, pr = blockIdx.x % pairs;
+  const int c = blockIdx.y, seq = blockIdx.z;
+  const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
+  if (c * L >= sp.len) return;
+  const int hs = threadIdx.x >> 7, t = threadIdx.x & 127, q = t >> 5, lane = t & 31;
+  const int h = g * hpg + pr * NH + hs;
+  const bool live = pr * NH + hs < hpg && c * L + t < sp.len;
+  float* vec = vecs + (((long)seq * gridDim.x + blockIdx.x) * gridDim.y + c) * (kVec / 4);
+  __shared__ float4 tot[NH];
+  float step = 0.f, pre = 0.f;
+  if (live) {
+    const float raw = __bfloat162float(static_cast<const bf16_t*>(a.dt)[(sp.row0 + c * L + t) * a.lddt + h]);
+    step = softplus(raw + (a.dt_bias ? a.dt_bias[h] : 0.f));
+    pre = step * (-expf(a.A_log[h]) * kLog2e);
+  }
+  float suf = pre;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float up = __shfl_up_sync(0xffffffffu, pre, o);
+    const float dn = __shfl_down_sync(0xffffffffu, suf, o);
+    if (lane >= o) pre += up;
+    if (lane < 32 - o) suf += dn;
+  }
+  suf = __shfl_down_sync(0xffffffffu, suf, 1);   // the sum over the tokens after this one
+  if (lane == 31) {
+    suf = 0.f;
+    reinterpret_cast<float*>(&tot[hs])[q] = pre;
+  }
+  __syncthreads();
+  const float4 s4 = tot[hs];
+  const float before = q == 0 ? 0.f : q == 1 ? s4.x : q == 2 ? s4.x + s4.y : s4.x + s4.y + s4.z;
+  const float after = q == 3 ? 0.f : q == 2 ? s4.w : q == 1 ? s4.z + s4.w : s4.y + s4.z + s4.w;
+  const int at = hs * 128 + t;
+  vec[VU + at] = step * tc::ex2(suf);
+  vec[VW + at] = step * tc::ex2(suf + after);
+  vec[VE + at] = tc::ex2(pre + before);
+  vec[VP + at] = pre;
+  vec[VP + 256 + at] = pre - log2_step(step);
+  if (t == 0) {
+    *reinterpret_cast<float4*>(vec + VT + hs * 4) = s4;
+    vec[VD + hs] = tc::ex2(s4.x + s4.y + s4.z + s4.w);
+  }
 }
 
 template <int N, int P, bool kOut>
@@ -158,7 +264,8 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = tc::smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be uniform)
 
   const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH;
   const int g = blockIdx.x / pairs, pr = blockIdx.x % pairs;
@@ -178,7 +285,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::bars + kBars * 8 + 8);
   auto bar = [&](int i) { return sb + Lay::bars + 8u * i; };
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(tc::smem_u32(&bars[i]), i >= XT0 && i <= YR ? 128 : 1);
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(tc::smem_u32(&bars[i]), i == DRAIN ? (kOut ? 2 : 1) : i == YR ? 256 : i >= XT ? 128 : 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -194,284 +301,249 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto wait = [&](int b, int phase) { tc::mbar_wait(bar(b), (uint32_t)phase & 1u, abort_flag, kBudget); };
+  auto wait = [&](int b, int phase) { bounded_wait(bar(b), (uint32_t)phase & 1u, abort_flag); };
   const int row0 = (int)(sp.row0 + (long)ch0 * L);        // this segment's first row
   const int wg = warp >> 2, q = warp & 3;                 // warpgroup; lane quadrant
   const int t = tid & 127;                                // a token's (or hp's) row
   const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
   auto vec_of = [&](int c) { return reinterpret_cast<float*>(smem + Lay::vec + (c % 3) * kVec); };
-  // a chunk's vectors: u [2][128] D_s exp(suffix in its block), w [2][128] D_s exp(suffix in the chunk), e [2][128]
-  // exp(prefix in the chunk), prefix in its block [2][128], the same less log2 D_s [2][128], block sums [2][4], exp(chunk's sum) [2]
-  constexpr int VU = 0, VW = 256, VE = 512, VP = 768, VT = 1280, VD = 1288;
 
   if (wg == 0) {
-    regs_dec<80>();          // 80 + 96 + 208 + 128: the 512 registers of four threads at launch
-    if (lane == 0 && nc > 0) {
-      volatile int never = 0;
-      if (warp == 0) {
-        // --------------------------------- B and C ---------------------------------------------
-        auto load_n = [&](uint32_t dst, const CUtensorMap* m, int b, int c) {
-          tc::mbar_arrive_expect_tx(bar(b), NB * kTile);
-          for (int i = 0; i < NB; ++i) tma_load_2d(dst + i * kTile, m, bar(b), g * N + i * 64, row0 + c * L);
-        };
-        int bs = 0, cs = 0;                   // loads issued
-        auto load_b = [&] {
-          const int buf = kOut ? 0 : bs & 1;
-          load_n(sb + Lay::b + buf * NB * kTile, &mb, BF + buf, bs);
-          ++bs;
-        };
-        load_b();
-        if (kOut) load_n(sb + Lay::c, &mc, CF, cs++);
-        else if (nc > 1) load_b();
-        for (int c = 0; c < nc && !*abort_flag; ++c) {
-          if (kOut) wait(U1, c);
-          else wait(BE + (c & 1), c >> 1);
-          if (bs < nc) load_b();
-          if (kOut && cs < nc) {
-            wait(YI, c);
-            load_n(sb + Lay::c, &mc, CF, cs++);
-          }
-        }
-        // every load issued lands before the CTA can leave
+    regs_dec<56>();          // 56 + 72 + 192 + 2 x 80: the registers of five threads at launch (96 each)
+    volatile int never = 0;
+    if (warp == 0 && lane == 0 && nc > 0) {
+      // ------------------------------- B, C and the decay vectors ------------------------------
+      auto load_n = [&](uint32_t dst, const CUtensorMap* m, int b, int c) {
+        tc::mbar_arrive_expect_tx(bar(b), NB * kTile);
+#pragma unroll 1
+        for (int i = 0; i < NB; ++i) tma_load_2d(dst + i * kTile, m, bar(b), g * N + i * 64, row0 + c * L);
+      };
+      int bs = 0, cs = 0, vs = 0;             // loads issued
+      auto load_b = [&] {
+        const int buf = kOut ? 0 : bs & 1;
+        load_n(sb + Lay::b + buf * NB * kTile, &mb, BF + buf, bs);
+        ++bs;
+      };
+      const float* src = k.vecs + (((long)seq * gridDim.x + blockIdx.x) * k.chunks + ch0) * (kVec / 4);
+      auto load_v = [&] {
+        tc::mbar_arrive_expect_tx(bar(VR + vs % 3), kVec);
+        tc::bulk_load(sb + Lay::vec + (vs % 3) * kVec, src + (long)vs * (kVec / 4), kVec, bar(VR + vs % 3));
+        ++vs;
+      };
+#pragma unroll 1
+      while (vs < nc && vs < 3) load_v();
+#pragma unroll 1
+      while (bs < nc && bs < (kOut ? 1 : 2)) load_b();
+      if (kOut) load_n(sb + Lay::c, &mc, CF, cs++);
+#pragma unroll 1
+      for (int c = 0; c < nc && !*abort_flag; ++c) {
         if (kOut) {
-          tc::mbar_wait(bar(BF), (bs - 1) & 1, &never, kBudget / 4);
-          tc::mbar_wait(bar(CF), (cs - 1) & 1, &never, kBudget / 4);
+          wait(GD, c);                        // both have read B
+          wait(U1, c);
         } else {
-          for (int i = max(0, bs - 2); i < bs; ++i) tc::mbar_wait(bar(BF + (i & 1)), (i >> 1) & 1, &never, kBudget / 4);
+          wait(BE + (c & 1), c >> 1);
         }
-      } else if (warp == 2) {
-        // --------------------------------- x and y ---------------------------------------------
-        if constexpr (kOut) {
-          int xs = 0;
-          auto load_x = [&] {
-            const uint32_t dst = sb + Lay::x + (xs & 1) * 2 * kTile, b = bar(XF + (xs & 1));
-            tc::mbar_arrive_expect_tx(b, (NH == 2 && heads == 1 ? 1 : 2) * kTile);
-            tma_load_2d(dst, &mx, b, h0 * P, row0 + xs * L);
-            if (NH == 1 || heads == 2) tma_load_2d(dst + kTile, &mx, b, h0 * P + 64, row0 + xs * L);
-            ++xs;
-          };
-          load_x();
-          if (nc > 1) load_x();
-          for (int c = 0; c < nc && !*abort_flag; ++c) {
-            wait(YR, c);
-            if (sp.len - (ch0 + c) * L >= L) {
-              const uint32_t src = sb + Lay::x + (c & 1) * 2 * kTile;
-              tma_store_2d(&my, src, h0 * P, row0 + c * L);
-              if (NH == 1 || heads == 2) tma_store_2d(&my, src + kTile, h0 * P + 64, row0 + c * L);
-              tc::bulk_commit();
-            }
-            if (xs < nc) {
-              tc::bulk_wait_read_all();
-              load_x();
-            }
-          }
-          tc::bulk_wait_all();                // every store has read its source before the CTA can leave
-          for (int i = max(0, xs - 2); i < xs; ++i) tc::mbar_wait(bar(XF + (i & 1)), (i >> 1) & 1, &never, kBudget / 4);
+        if (bs < nc) load_b();
+        if (kOut) {
+          wait(YI, c);
+          if (cs < nc) load_n(sb + Lay::c, &mc, CF, cs++);
         }
-      } else if (warp == 1) {
-        // ----------------------------------- MMAs ----------------------------------------------
-        constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, false, false);
-        constexpr uint32_t ID_YA = tc::idesc_bf16(128, P, false, true);
-        constexpr uint32_t ID_U = tc::idesc_bf16(128, N, true, true);
-        const uint64_t dc = tc::sdesc_sw128(sb + Lay::c, 16, 1024);          // C, K = n
-        const uint64_t db = tc::sdesc_sw128(sb + Lay::b, 16, 1024);          // B, K = n
-        const uint64_t ds = tc::sdesc_sw128(sb + Lay::s, 16, 1024);          // S^T, K = n
-        auto spin = [&](int b, int phase) { tc::mbar_wait_spin(bar(b), (uint32_t)phase & 1u, abort_flag, kBudget); };
-        for (int c = 0; c < nc; ++c) {
-          const int bbuf = kOut ? 0 : c & 1;
-          const uint64_t dbt = tc::sdesc_sw128(sb + Lay::b + bbuf * NB * kTile, kTile, 1024);   // B, K = t
-          // half `hf` of the chunk's tokens: 4 steps of 16 for each of the three terms
-          auto issue_u = [&](int hf) {
-            const uint64_t dw = tc::sdesc_sw128(sb + Lay::xw + (kOut ? 0 : hf) * Lay::xw_stage, kTile / 2, 1024);
-#pragma unroll 1
-            for (int term = 0; term < 3; ++term)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                tc::mma_bf16(tmem + TU, tc::desc_adv(dw, term * kTile + i * 2048),
-                             tc::desc_adv(dbt, hf * (kTile / 2) + i * 2048), ID_U, hf + term + i > 0);
-          };
-          spin(BF + bbuf, kOut ? c : c >> 1);
-          spin(XT0, c);
-          if (c > 0) spin(UR, c - 1);
-          tc::tc_fence_after();
-          issue_u(0);
-          tc::mma_commit(bar(U0));
-          if constexpr (kOut) {
-            spin(CF, c);
-            tc::tc_fence_after();
-#pragma unroll 4
-            for (int i = 0; i < NB * 4; ++i) {
-              const uint32_t o = (i >> 2) * kTile + (i & 3) * 32;
-              tc::mma_bf16(tmem + TG, tc::desc_adv(dc, o), tc::desc_adv(db, o), ID_G, i > 0);
-            }
-            tc::mma_commit(bar(GD));
-          }
-          spin(XT1, c);
-          tc::tc_fence_after();
-          issue_u(1);
-          tc::mma_commit(bar(U1));
-          if constexpr (!kOut) tc::mma_commit(bar(BE + bbuf));
-          if constexpr (kOut) {
-            spin(SR, c);
-            if (c > 0) spin(YR, c - 1);
-            tc::tc_fence_after();
-#pragma unroll 4
-            for (int i = 0; i < NB * 4; ++i) {
-              const uint32_t o = (i >> 2) * kTile + (i & 3) * 32;
-              tc::mma_bf16(tmem + TYI, tc::desc_adv(dc, o), tc::desc_adv(ds, o), ID_G, i > 0);
-            }
-            tc::mma_commit(bar(YI));
-            spin(XF + (c & 1), c >> 1);
-            spin(PR, c);
-            tc::tc_fence_after();
-            const uint64_t dx = tc::sdesc_sw128(sb + Lay::x + (c & 1) * 2 * kTile, kTile, 1024);
-#pragma unroll 1
-            for (int hs = 0; hs < NH; ++hs)
-#pragma unroll 4
-              for (int i = 0; i < 8; ++i)
-                mma_bf16_ta(tmem + TYA + hs * 64, tmem + TG + 32 * (i >> 1) + 16 * hs + 8 * (i & 1),
-                            tc::desc_adv(dx, hs * kTile + i * 2048), ID_YA, i > 0);
-            tc::mma_commit(bar(YA));
-          }
-        }
-        tc::mma_commit(bar(DRAIN));
-        tc::mbar_wait(bar(DRAIN), 0, &never, kBudget / 4);
+        // the slot of chunk c - 1: U(c) was issued after its state, Yi(c) after its y
+        if (c >= 1 && vs < nc) load_v();
       }
+      // every load issued lands before the CTA can leave
+      if (kOut) {
+        bounded_wait(bar(BF), (bs - 1) & 1, &never);
+        bounded_wait(bar(CF), (cs - 1) & 1, &never);
+      } else {
+        for (int i = max(0, bs - 2); i < bs; ++i) bounded_wait(bar(BF + (i & 1)), (i >> 1) & 1, &never);
+      }
+      for (int i = max(0, vs - 3); i < vs; ++i) bounded_wait(bar(VR + i % 3), (i / 3) & 1, &never);
+    } else if (warp == 2 && lane == 0 && nc > 0) {
+      // --------------------------------- x and y -----------------------------------------------
+      if constexpr (kOut) {
+        int xs = 0;
+        auto load_x = [&] {
+          const uint32_t dst = sb + Lay::x + (xs & 1) * 2 * kTile, b = bar(XF + (xs & 1));
+          tc::mbar_arrive_expect_tx(b, (NH == 2 && heads == 1 ? 1 : 2) * kTile);
+          tma_load_2d(dst, &mx, b, h0 * P, row0 + xs * L);
+          if (NH == 1 || heads == 2) tma_load_2d(dst + kTile, &mx, b, h0 * P + 64, row0 + xs * L);
+          ++xs;
+        };
+#pragma unroll 1
+        while (xs < nc && xs < 2) load_x();
+#pragma unroll 1
+        for (int c = 0; c < nc && !*abort_flag; ++c) {
+          wait(YR, c);
+          if (sp.len - (ch0 + c) * L >= L) {
+            const uint32_t src = sb + Lay::x + (c & 1) * 2 * kTile;
+            tma_store_2d(&my, src, h0 * P, row0 + c * L);
+            if (NH == 1 || heads == 2) tma_store_2d(&my, src + kTile, h0 * P + 64, row0 + c * L);
+            tc::bulk_commit();
+          }
+          if (xs < nc) {
+            tc::bulk_wait_read_all();
+            load_x();
+          }
+        }
+        tc::bulk_wait_all();                  // every store has read its source before the CTA can leave
+        for (int i = max(0, xs - 2); i < xs; ++i) bounded_wait(bar(XF + (i & 1)), (i >> 1) & 1, &never);
+      }
+    } else if (warp == 3 && nc > 0) {
+      // ----------------------------------- MMAs of U -------------------------------------------
+      const uint32_t leader = elect();
+      constexpr uint32_t ID_U = tc::idesc_bf16(128, N, true, true);
+      const uint64_t dxw = tc::sdesc_sw128(sb + Lay::xw, kTile / 4, 1024);                      // X', K = t
+      const uint64_t db0 = tc::sdesc_sw128(sb + Lay::b, kTile, 1024);                           // B, K = t
+#pragma unroll 1
+      for (int c = 0; c < nc; ++c) {
+        const int bbuf = kOut ? 0 : c & 1;
+        const uint64_t dbt = tc::desc_adv(db0, bbuf * NB * kTile);
+        wait(BF + bbuf, kOut ? c : c >> 1);
+        if (c > 0) wait(UR, c - 1);
+        // a quarter of the chunk's tokens: 2 steps of 16 for each of the three terms
+#pragma unroll 1
+        for (int qd = 0; qd < 4; ++qd) {
+          wait(XT + (qd & 1), 2 * c + (qd >> 1));
+          tc::tc_fence_after();
+          const uint64_t dw = tc::desc_adv(dxw, (qd & 1) * kSlot), dq = tc::desc_adv(dbt, qd * (kTile / 4));
+#pragma unroll
+          for (int i = 0; i < 6; ++i)
+            mma_ss(tmem + TU, tc::desc_adv(dw, (i >> 1) * (kTile / 2) + (i & 1) * 2048), tc::desc_adv(dq, (i & 1) * 2048),
+                   ID_U, qd + i > 0, leader);
+          commit(bar(UQ + (qd & 1)), leader);
+        }
+        commit(bar(U1), leader);
+        if (!kOut) commit(bar(BE + bbuf), leader);
+      }
+      commit(bar(DRAIN), leader);
+      bounded_wait(bar(DRAIN), 0, &never);
+    } else if (kOut && warp == 1 && nc > 0) {
+      // ----------------------------------- MMAs of G, Yi, Ya -----------------------------------
+      const uint32_t leader = elect();
+      constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, false, false);
+      constexpr uint32_t ID_YA = tc::idesc_bf16(128, P, false, true);
+      const uint64_t dc = tc::sdesc_sw128(sb + Lay::c, 16, 1024);          // C, K = n
+      const uint64_t db = tc::sdesc_sw128(sb + Lay::b, 16, 1024);          // B, K = n
+      const uint64_t ds = tc::sdesc_sw128(sb + Lay::s, 16, 1024);          // S^T, K = n
+      const uint64_t dx0 = tc::sdesc_sw128(sb + Lay::x, kTile, 1024);      // x, K = t
+#pragma unroll 1
+      for (int c = 0; c < nc; ++c) {
+        wait(BF, c);
+        wait(CF, c);
+        // G = C B^T, then Yi = C S
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          if (w) {
+            wait(SR, c);
+            if (c > 0) wait(YR, c - 1);
+          }
+          tc::tc_fence_after();
+          const uint64_t dn = w ? ds : db;
+#pragma unroll 1
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_ss(tmem + (w ? TYI : TG), tc::desc_adv(dc, n * kTile + i * 32), tc::desc_adv(dn, n * kTile + i * 32), ID_G,
+                     n + i > 0, leader);
+          commit(bar(w ? YI : GD), leader);
+        }
+        wait(XF + (c & 1), c >> 1);
+        wait(PR, c);
+        tc::tc_fence_after();
+        const uint64_t dx = tc::desc_adv(dx0, (c & 1) * 2 * kTile);
+#pragma unroll 1
+        for (int hs = 0; hs < NH; ++hs)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            mma_ts(tmem + TYA + hs * 64, tmem + TG + 32 * (i >> 1) + 16 * hs + 8 * (i & 1),
+                   tc::desc_adv(dx, hs * kTile + i * 2048), ID_YA, i > 0, leader);
+        commit(bar(YA), leader);
+      }
+      commit(bar(DRAIN), leader);
+      bounded_wait(bar(DRAIN), 0, &never);
     }
   } else if (wg == 1 || (!kOut && wg == 3)) {
-    // ------------------------- the decays and X' (without outputs: a half each) ------------------
-    if (wg == 1) regs_dec<96>();
-    float rate[NH], bias[NH];
-#pragma unroll
-    for (int hs = 0; hs < NH; ++hs) {
-      rate[hs] = hs < heads ? -expf(a.A_log[h0 + hs]) * kLog2e : 0.f;
-      bias[hs] = hs < heads && a.dt_bias ? a.dt_bias[h0 + hs] : 0.f;
-    }
-    const bf16_t* dtp = static_cast<const bf16_t*>(a.dt) + h0;
+    // ------------------------- X' (without outputs: every other quarter each) --------------------
+    regs_dec<72>();
     const bf16_t* xp = static_cast<const bf16_t*>(a.x) + (long)h0 * P;
-    bf16_t raw[NH];                  // kept as loaded: a conversion would wait for the load at once
-    auto load_dt = [&](int c) {
-      const int at = (ch0 + c) * L + t;
-#pragma unroll
-      for (int hs = 0; hs < NH; ++hs)
-        if (hs < heads && c < nc && at < sp.len) raw[hs] = dtp[(sp.row0 + at) * a.lddt + hs];
-    };
-    // this thread's eight 16-byte pieces of a half: rows (t + 128 i) / 16, piece t % 16 of 16
+    // this thread's four 16-byte pieces of a quarter: rows (t + 128 i) / 16, piece t % 16 of 16
     const int j = t & 7, tile = (t >> 3) & 1, r0 = t >> 4;
-    uint4 xv[8];
-    auto load_x = [&](int c, int hf) {
-      const int at = (ch0 + c) * L + hf * 64 + r0;
+    constexpr int kStep = kOut ? 1 : 2;           // quarters from one of this warpgroup's to its next
+    const int q0 = wg == 1 ? 0 : 1;
+    uint4 xa[4], xb[4];                           // this quarter's pieces and the next one's: each is loaded a quarter
+    auto load_x = [&](int qq, uint4 (&xv)[4]) {   // ahead and touched by nothing before its use (a move would wait)
+      const int at = ch0 * L + qq * 32 + r0;
       const bf16_t* p = xp + (sp.row0 + at) * a.ldx + tile * 64 + j * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         xv[i] = make_uint4(0, 0, 0, 0);
-        if (c < nc && at + 8 * i < sp.len && (NH == 1 || tile < heads))
+        if (qq < 4 * nc && at + 8 * i < sp.len && (NH == 1 || tile < heads))
           xv[i] = *reinterpret_cast<const uint4*>(p + (long)(8 * i) * a.ldx);
       }
     };
-    load_dt(0);
-    load_x(0, kOut || wg == 1 ? 0 : 1);
-    for (int c = 0; c < nc; ++c) {
-      float* vec = vec_of(c);
-      const int valid = min(L, sp.len - (ch0 + c) * L);
-      // ---- decays, in base-2 logarithms.  Their slot held chunk c - 3's: with outputs this thread has seen U0
-      // of chunk c - 1, issued after Yi of c - 2 and so after every reader of c - 3; without, U0 or U1 of c - 2.
-      float pre[NH], suf[NH], step[NH];
-#pragma unroll
-      for (int hs = 0; hs < NH; ++hs) {
-        step[hs] = t < valid && hs < heads ? softplus(__bfloat162float(raw[hs]) + bias[hs]) : 0.f;
-        pre[hs] = suf[hs] = t < valid ? step[hs] * rate[hs] : 0.f;
-      }
-      load_dt(c + 1);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-        for (int hs = 0; hs < NH; ++hs) {
-          const float up = __shfl_up_sync(0xffffffffu, pre[hs], o);
-          const float dn = __shfl_down_sync(0xffffffffu, suf[hs], o);
-          if (lane >= o) pre[hs] += up;
-          if (lane < 32 - o) suf[hs] += dn;
+    auto quarter = [&](int qq, uint4 (&xv)[4]) {
+      const int c = qq >> 2, qd = qq & 3, slot = qd & 1;
+      const float* vec = vec_of(c);
+      if (qd < kStep) {
+        wait(VR + c % 3, c / 3);
+        // the next chunk's rows into L2: the loads a quarter ahead then take no longer than a quarter
+        const int at = (ch0 + c + 1) * L + t;
+        if (c + 1 < nc && at < sp.len) {
+          const bf16_t* p = xp + (sp.row0 + at) * a.ldx;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+          if (NH == 1 || heads == 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64));
         }
       }
-#pragma unroll
-      for (int hs = 0; hs < NH; ++hs) {
-        suf[hs] = __shfl_down_sync(0xffffffffu, suf[hs], 1);   // the sum over the tokens after this one
-        if (lane == 31) {
-          suf[hs] = 0.f;
-          vec[VT + hs * 4 + q] = pre[hs];
-        }
-        vec[VP + hs * 128 + t] = pre[hs];
-        vec[VP + 256 + hs * 128 + t] = pre[hs] - log2_step(step[hs]);
-        vec[VU + hs * 128 + t] = step[hs] * tc::ex2(suf[hs]);
-      }
-      tc::named_bar(wg, 128);
-#pragma unroll
-      for (int hs = 0; hs < NH; ++hs) {
-        const float4 s4 = *reinterpret_cast<const float4*>(vec + VT + hs * 4);
-        const float before = q == 0 ? 0.f : q == 1 ? s4.x : q == 2 ? s4.x + s4.y : s4.x + s4.y + s4.z;
-        const float after = q == 3 ? 0.f : q == 2 ? s4.w : q == 1 ? s4.z + s4.w : s4.y + s4.z + s4.w;
-        vec[VW + hs * 128 + t] = step[hs] * tc::ex2(suf[hs] + after);
-        vec[VE + hs * 128 + t] = tc::ex2(pre[hs] + before);
-        if (t == 0) vec[VD + hs] = tc::ex2(s4.x + s4.y + s4.z + s4.w);
-      }
-      tc::named_bar(wg, 128);
-      if (kOut && valid < L) {   // rows behind the sequence reach no product: another sequence's, maybe NaN
-        // (G may be reading B meanwhile: it yields columns s >= valid, which no row t < valid keeps)
-        wait(XF + (c & 1), c >> 1);
-        wait(BF, c);
-        const uint32_t xt = sb + Lay::x + (c & 1) * 2 * kTile;
-        for (int i = t; i < (L - valid) * 8 * (2 + NB); i += 128) {
-          const int jj = i & 7, tl = (i >> 3) % (2 + NB), r = valid + (i >> 3) / (2 + NB);
-          tc::st_shared_v4((tl < 2 ? xt + tl * kTile : sb + Lay::b + (tl - 2) * kTile) + tc::sw128(r, jj), 0, 0, 0, 0);
+      if (kOut && qd == 0) {
+        const int valid = min(L, sp.len - (ch0 + c) * L);
+        if (valid < L) {     // rows behind the sequence reach no product: another sequence's, maybe NaN
+          // (G may be reading B meanwhile: it yields columns s >= valid, which no row t < valid keeps)
+          wait(BF, c);
+          zero_rows(sb + Lay::b, NB, valid, t);
         }
       }
-      // ---- X' of half `hf`: three bf16 terms that add up to the fp32 product.  (The loops of the roles are kept
-      // rolled where registers allow: four roles of unrolled code do not fit the instruction cache.)
+      if (qq >= 2) wait(UQ + slot, (qq >> 1) - 1);      // the slot is free again
+      // three bf16 terms that add up to the fp32 product
+      const uint32_t dst = sb + Lay::xw + slot * kSlot + tile * (kTile / 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 8 * i;
+        const float w = vec[VW + (NH == 2 ? tile : 0) * 128 + qd * 32 + r];
+        const uint64_t ww = tc::f2(w, w);
+        const uint32_t in[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+        uint32_t o0[4], o1[4], o2[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t f = tc::mul2(tc::f2(tc::bf16lo(in[e]), tc::bf16hi(in[e])), ww);
+          float f0, f1;
+          tc::f2_get(f, f0, f1);
+          o0[e] = tc::pack_bf16(f0, f1);
+          const uint64_t g2 = tc::sub2(f, tc::f2(tc::bf16lo(o0[e]), tc::bf16hi(o0[e])));
+          tc::f2_get(g2, f0, f1);
+          o1[e] = tc::pack_bf16(f0, f1);
+          tc::f2_get(tc::sub2(g2, tc::f2(tc::bf16lo(o1[e]), tc::bf16hi(o1[e]))), f0, f1);
+          o2[e] = tc::pack_bf16(f0, f1);
+        }
+        const uint32_t at = dst + tc::sw128(r, j);
+        tc::st_shared_v4(at, o0[0], o0[1], o0[2], o0[3]);
+        tc::st_shared_v4(at + kTile / 2, o1[0], o1[1], o1[2], o1[3]);
+        tc::st_shared_v4(at + kTile, o2[0], o2[1], o2[2], o2[3]);
+      }
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive(bar(XT + slot));
+      load_x(qq + 2 * kStep, xv);
+    };
+    load_x(q0, xa);
+    load_x(q0 + kStep, xb);
 #pragma unroll 1
-      for (int hh = 0; hh < (kOut ? 2 : 1); ++hh) {
-        const int hf = kOut ? hh : (wg == 1 ? 0 : 1);
-        const uint32_t dst = sb + Lay::xw + (kOut ? 0 : hf) * Lay::xw_stage + tile * (kTile / 2);
-        // the staging is free again
-        if (kOut && hf) wait(U0, c);
-        else if (c > 0) wait(kOut || hf ? U1 : U0, c - 1);
-#pragma unroll 1
-        for (int i2 = 0; i2 < 4; ++i2) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = r0 + 8 * (2 * i2 + i);
-          const float w = vec[VW + (NH == 2 ? tile : 0) * 128 + hf * 64 + r];
-          const uint64_t ww = tc::f2(w, w);
-          const uint32_t in[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
-          uint32_t o0[4], o1[4], o2[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint64_t f = tc::mul2(tc::f2(tc::bf16lo(in[e]), tc::bf16hi(in[e])), ww);
-            float f0, f1;
-            tc::f2_get(f, f0, f1);
-            o0[e] = tc::pack_bf16(f0, f1);
-            const uint64_t g2 = tc::sub2(f, tc::f2(tc::bf16lo(o0[e]), tc::bf16hi(o0[e])));
-            tc::f2_get(g2, f0, f1);
-            o1[e] = tc::pack_bf16(f0, f1);
-            tc::f2_get(tc::sub2(g2, tc::f2(tc::bf16lo(o1[e]), tc::bf16hi(o1[e]))), f0, f1);
-            o2[e] = tc::pack_bf16(f0, f1);
-          }
-          const uint32_t at = dst + tc::sw128(r, j);
-          tc::st_shared_v4(at, o0[0], o0[1], o0[2], o0[3]);
-          tc::st_shared_v4(at + kTile, o1[0], o1[1], o1[2], o1[3]);
-          tc::st_shared_v4(at + 2 * kTile, o2[0], o2[1], o2[2], o2[3]);
-        }
-#pragma unroll
-        for (int i = 0; i < 6; ++i) xv[i] = xv[i + 2];
-        }
-        tc::fence_proxy_async_smem();
-        tc::mbar_arrive(bar(hf ? XT1 : XT0));
-        if (kOut) load_x(c + hh, hh ^ 1);            // the next half: of this chunk, then of the next
-        else load_x(c + 1, hf);
-      }
+    for (int qq = q0; qq < 4 * nc; qq += 2 * kStep) {   // a chunk's quarters of this warpgroup are two or four
+      quarter(qq, xa);
+      quarter(qq + kStep, xb);
     }
   } else if (wg == 2) {
     // ----------------------------------- P and the state -----------------------------------------
-    regs_inc<208>();
+    regs_inc<192>();
     const int sh = NH == 2 ? (t >> 6) : 0;           // the head of state row t
     const int p = NH == 2 ? (t & 63) : t;
     const bool s_on = sh < heads;
@@ -509,30 +581,31 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     for (int c = 0; c < nc; ++c) {
       const float* vec = vec_of(c);
       if constexpr (kOut) {
-        // ---- P from G, block of 32 columns by block
+        // ---- P from G
         wait(GD, c);
         tc::tc_fence_after();
+        float mid[NH], mine[NH];
+#pragma unroll
+        for (int hs = 0; hs < NH; ++hs) mid[hs] = mine[hs] = vec[VP + hs * 128 + t];
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 3; b >= 0; --b) {
+          const uint32_t at = tlane + TG + 32 * b;
           if (b > q) {                               // after every token of these rows
             uint32_t o[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = 0;
-#pragma unroll
-            for (int hs = 0; hs < NH; ++hs) tmem_st16(tlane + TG + 32 * b + 16 * hs, o);
+            tmem_st16(at, o);
+            if (NH == 2) tmem_st16(at + 16, o);
             continue;
           }
           float G[32];
-          tc::tmem_ld32(tlane + TG + 32 * b, G);
+          tc::tmem_ld32(at, G);
           tc::tmem_wait_ld();
 #pragma unroll 1
           for (int hs = 0; hs < NH; ++hs) {
             uint32_t o[16];
-            const float mine = vec[VP + hs * 128 + t];
             if (b < q) {
-              float mid = mine;
-              for (int i = b + 1; i < q; ++i) mid += vec[VT + hs * 4 + i];
-              const float r = tc::ex2(mid);
+              const float r = tc::ex2(hs ? mid[NH - 1] : mid[0]);
               const uint64_t rr = tc::f2(r, r);
               const float4* u4 = reinterpret_cast<const float4*>(vec + VU + hs * 128 + 32 * b);
 #pragma unroll
@@ -545,22 +618,33 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
                 o[2 * i + 1] = tc::pack_bf16(f0, f1);
               }
             } else {
+              const float m = hs ? mine[NH - 1] : mine[0];
               const float4* p4 = reinterpret_cast<const float4*>(vec + VP + 256 + hs * 128 + 32 * b);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const float4 v = p4[i];              // prefix - log2 D of columns 4 i .. 4 i + 3
-                const float f0 = 4 * i <= lane ? G[4 * i] * tc::ex2(mine - v.x) : 0.f;
-                const float f1 = 4 * i + 1 <= lane ? G[4 * i + 1] * tc::ex2(mine - v.y) : 0.f;
-                const float f2 = 4 * i + 2 <= lane ? G[4 * i + 2] * tc::ex2(mine - v.z) : 0.f;
-                const float f3 = 4 * i + 3 <= lane ? G[4 * i + 3] * tc::ex2(mine - v.w) : 0.f;
+                const float f0 = 4 * i <= lane ? G[4 * i] * tc::ex2(m - v.x) : 0.f;
+                const float f1 = 4 * i + 1 <= lane ? G[4 * i + 1] * tc::ex2(m - v.y) : 0.f;
+                const float f2 = 4 * i + 2 <= lane ? G[4 * i + 2] * tc::ex2(m - v.z) : 0.f;
+                const float f3 = 4 * i + 3 <= lane ? G[4 * i + 3] * tc::ex2(m - v.w) : 0.f;
                 o[2 * i] = tc::pack_bf16(f0, f1);
                 o[2 * i + 1] = tc::pack_bf16(f2, f3);
               }
             }
-            tmem_st16(tlane + TG + 32 * b + 16 * hs, o);
+            tmem_st16(at + 16 * hs, o);
+          }
+          if (b < q) {                               // the blocks between: whole
+#pragma unroll
+            for (int hs = 0; hs < NH; ++hs) mid[hs] += vec[VT + hs * 4 + b];
           }
         }
         tc::tmem_wait_st();
+        const int valid = min(L, sp.len - (ch0 + c) * L);
+        if (valid < L) {                             // nor do x's rows behind the sequence reach Ya
+          wait(XF + (c & 1), c >> 1);
+          zero_rows(sb + Lay::x + (c & 1) * 2 * kTile, 2, valid, t);
+          tc::fence_proxy_async_smem();
+        }
         tc::tc_fence_before();
         tc::mbar_arrive(bar(PR));
       }
@@ -602,55 +686,48 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     }
   } else {
     // ------------------------------------------- y -----------------------------------------------
+    regs_dec<80>();
     if constexpr (kOut) {
-      float skip[NH];
-#pragma unroll
-      for (int hs = 0; hs < NH; ++hs) skip[hs] = a.D && hs < heads ? a.D[h0 + hs] : 0.f;
+      const int half = wg - 3;                       // this warpgroup's 64 columns
+      const int hs = NH == 2 ? half : 0;             // their head
+      const bool y_on = hs < heads;
+      const float skip = a.D && y_on ? a.D[h0 + hs] : 0.f;
+      const uint64_t skip2 = tc::f2(skip, skip);
       const bool gated = a.z != nullptr;
       for (int c = 0; c < nc; ++c) {
         const int valid = min(L, sp.len - (ch0 + c) * L);
         const long row = (long)row0 + c * L + t;
         const uint32_t xt = sb + Lay::x + (c & 1) * 2 * kTile;
-        const bf16_t* zp = gated ? static_cast<const bf16_t*>(a.z) + row * a.ldz + (long)h0 * P : nullptr;
-        bf16_t* yp = static_cast<bf16_t*>(a.y) + row * ((long)a.H * P) + (long)h0 * P;
-        // the gate's values of 16 columns (piece i of eight)
+        const bf16_t* zp = gated ? static_cast<const bf16_t*>(a.z) + row * a.ldz + (long)h0 * P + 64 * half : nullptr;
+        bf16_t* yp = static_cast<bf16_t*>(a.y) + row * ((long)a.H * P) + (long)h0 * P + 64 * half;
+        // the gate's values of 16 columns (piece i of this warpgroup's four)
         auto load_z = [&](int i, uint4 (&zr)[2]) {
-          const bool on = gated && t < valid && (NH == 1 || (i >> 2) < heads);
+          const bool on = gated && t < valid && y_on;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             zr[e] = make_uint4(0, 0, 0, 0);
             if (!on) continue;
-            const bf16_t* zq = zp + 16 * i + 8 * e;
-            if (k.z_vec) {
-              zr[e] = *reinterpret_cast<const uint4*>(zq);
-            } else {
-              uint32_t v[4];
-#pragma unroll
-              for (int f = 0; f < 4; ++f)
-                v[f] = (uint32_t)__bfloat16_as_ushort(zq[2 * f]) | ((uint32_t)__bfloat16_as_ushort(zq[2 * f + 1]) << 16);
-              zr[e] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
+            zr[e] = *reinterpret_cast<const uint4*>(zp + 16 * i + 8 * e);
           }
         };
         uint4 zr[2];
         load_z(0, zr);
+        if (gated && y_on && c + 1 < nc && (ch0 + c + 1) * L + t < sp.len)     // the next chunk's into L2
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(zp + L * a.ldz));
         wait(XF + (c & 1), c >> 1);
         wait(YA, c);
         tc::tc_fence_after();
+        const float e = vec_of(c)[VE + hs * 128 + t];
+        const uint64_t e2 = tc::f2(e, e);
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          const int hs = NH == 2 ? i >> 2 : 0;
-          const float dskip = NH == 2 && hs ? skip[NH - 1] : skip[0];
-          if (NH == 2 && hs >= heads) break;
-          const float e = vec_of(c)[VE + hs * 128 + t];
+        for (int i = 0; i < 4 && y_on; ++i) {
           float yi[16], ya[16];
-          tmem_ld16(tlane + TYI + 16 * i, yi);
-          tmem_ld16(tlane + TYA + 16 * i, ya);
-          const uint32_t at0 = xt + (i >> 2) * kTile + tc::sw128(t, 2 * (i & 3));
-          const uint32_t at1 = xt + (i >> 2) * kTile + tc::sw128(t, 2 * (i & 3) + 1);
+          tmem_ld16(tlane + TYI + 64 * half + 16 * i, yi);
+          tmem_ld16(tlane + TYA + 64 * half + 16 * i, ya);
+          const uint32_t at0 = xt + half * kTile + tc::sw128(t, 2 * i), at1 = xt + half * kTile + tc::sw128(t, 2 * i + 1);
           const uint4 xq[2] = {tc::ld_shared_v4(at0), tc::ld_shared_v4(at1)};
           uint4 zn[2];
-          if (i < 7) load_z(i + 1, zn);
+          if (i < 3) load_z(i + 1, zn);
           tc::tmem_wait_ld();
           uint32_t o[2][4];
 #pragma unroll
@@ -660,12 +737,14 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
               const int col = 8 * m + 2 * f;
-              float f0 = fmaf(e, yi[col], fmaf(dskip, tc::bf16lo(xi[f]), ya[col]));
-              float f1 = fmaf(e, yi[col + 1], fmaf(dskip, tc::bf16hi(xi[f]), ya[col + 1]));
+              uint64_t y2 = tc::fma2(skip2, tc::f2(tc::bf16lo(xi[f]), tc::bf16hi(xi[f])), tc::f2(ya[col], ya[col + 1]));
+              y2 = tc::fma2(e2, tc::f2(yi[col], yi[col + 1]), y2);
               if (gated) {
-                f0 *= silu(tc::bf16lo(zi[f]));
-                f1 *= silu(tc::bf16hi(zi[f]));
+                const float z0 = tc::bf16lo(zi[f]), z1 = tc::bf16hi(zi[f]);
+                y2 = tc::mul2(y2, tc::mul2(tc::f2(z0, z1), tc::f2(sigmoid(z0), sigmoid(z1))));
               }
+              float f0, f1;
+              tc::f2_get(y2, f0, f1);
               o[m][f] = tc::pack_bf16(f0, f1);
             }
           }
@@ -738,24 +817,32 @@ inline int segments(int nseq, int max_len, int H, int G, int P) {
   const int s = (int)(fit < chunks / 4 ? fit : chunks / 4);
   return s < 2 ? 1 : s;
 }
-inline size_t workspace(int nseq, int max_len, int H, int G, int P, int N) {
-  const size_t s = (size_t)segments(nseq, max_len, H, G, P) - 1;
-  return (size_t)nseq * s * H * ((size_t)N * P + 1) * sizeof(float);
+// The workspace: segment states and decays, then the decay vectors.
+struct Space {
+  size_t vecs, bytes;
+};
+inline Space space(int nseq, int max_len, int H, int G, int P, int N) {
+  const size_t s = (size_t)segments(nseq, max_len, H, G, P) - 1, chunks = ((size_t)max_len + L - 1) / L;
+  const size_t states = ((size_t)nseq * s * H * ((size_t)N * P + 1) * sizeof(float) + 255) / 256 * 256;
+  return Space{states, states + (size_t)nseq * columns(H, G, P) * chunks * kVec};
 }
 
 template <int N, int P>
 int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
+  constexpr int NH = 128 / P;
   const long rows = a.cu ? (long)a.T : (long)a.nseq * a.T;
-  Args k{a, static_cast<float*>(ws), 0, segments(a.nseq, a.max_len, a.H, a.G, P), 0};
   const int chunks = (a.max_len + L - 1) / L;
-  k.seg_chunks = chunks > 0 ? (chunks + k.segments - 1) / k.segments : 1;
-  k.z_vec = a.z && a.ldz % 8 == 0 && (reinterpret_cast<uintptr_t>(a.z) & 15u) == 0;
+  const int segs = segments(a.nseq, a.max_len, a.H, a.G, P);
+  float* vecs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + space(a.nseq, a.max_len, a.H, a.G, P, N).vecs);
+  const Args k{a, static_cast<float*>(ws), vecs, chunks, (chunks + segs - 1) / segs, segs};
   CUtensorMap mx, mb, mc, my;
   if (!make_map(&mx, a.x, rows, (long)a.H * P, a.ldx) || !make_map(&mb, a.B, rows, (long)a.G * N, a.ldb) ||
       !make_map(&mc, a.C, rows, (long)a.G * N, a.ldc) || !make_map(&my, a.y, rows, (long)a.H * P, (long)a.H * P))
     return GDN_ERR_CUDA;
-  const dim3 grid((unsigned)columns(a.H, a.G, P), (unsigned)k.segments, (unsigned)a.nseq);
-  if (k.segments > 1) {
+  const dim3 grid((unsigned)columns(a.H, a.G, P), (unsigned)segs, (unsigned)a.nseq);
+  decay_kernel<NH><<<dim3(grid.x, (unsigned)chunks, grid.z), 128 * NH, 0, st>>>(a, vecs);
+  if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+  if (segs > 1) {
     auto first = scan_kernel<N, P, false>;
     if (cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, false>::alloc) != cudaSuccess)
       return GDN_ERR_CUDA;

@@ -612,8 +612,8 @@ GDN_API gdn_status gdn_ssm_conv_varlen(const void *x, long long ldx, const float
  *   S0 [B, H, N, P] float or NULL (zeros); y [B, T, H, P] (dtype, without gaps);
  *   S_T [B, H, N, P] float or NULL: the state after the last token (may not be S0's memory)
  *   workspace: gdn_ssm_scan_workspace_bytes(...) bytes, 256-byte aligned (NULL when that is 0)
- * bf16 with P and N in {64, 128}, 16-byte aligned x, Bm, Cm and ldx, ldb, ldc multiples of 8, run on
- * the tensor cores; everything else on the CUDA cores.  The state's updates are exact to fp32
+ * bf16 with P and N in {64, 128}, 16-byte aligned x, Bm, Cm, z and ldx, ldb, ldc, ldz multiples of 8,
+ * run on the tensor cores; everything else on the CUDA cores.  The state's updates are exact to fp32
  * rounding in both: the tensor-core kernel feeds them as three bf16 terms.
  */
 GDN_API gdn_status gdn_ssm_scan(const void *x, long long ldx, const void *dt, long long lddt,
