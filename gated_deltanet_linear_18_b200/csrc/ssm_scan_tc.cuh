@@ -87,8 +87,8 @@ template <int N, bool kOut> struct Layout {
   static_assert(alloc <= 232448, "shared memory of a CTA");
 };
 
-// Barriers.  By TMA: XF (two x tiles), BF (two B buffers), CF, VR (three vector slots).  By MMA commits: UQ (the two X' slots read), U1 (U
-// complete), BE (two B buffers free again), GD (G), YI, YA.  By the
+// Barriers.  By TMA: XF (two x tiles), BF (B's four quarters; without outputs two buffers), CF, VR (three vector slots).  By MMA commits: UQ (the two X' slots read), U1 (U
+// complete), BE (the same parts of B read by U), GD (G), YI, YA.  By the
 // threads of the warpgroups: XT (two X' slots staged), PR (P), UR (U is in registers), SR (the state operand), YR (y in
 // its tile, Yi and Ya read).
 // A wait names a phase by its parity alone, so each one below stands where the phase after the awaited
@@ -102,7 +102,7 @@ __device__ __forceinline__ float log2_step(float v) {
   return r;
 }
 
-enum Bar { XF = 0, BF = 2, CF = 4, UQ, U1 = UQ + 2, BE, GD = BE + 2, YI, YA, VR, DRAIN = VR + 3, XT, PR = XT + 2, UR, SR, YR, kBars };
+enum Bar { XF = 0, BF = 2, CF = BF + 4, UQ, U1 = UQ + 2, BE, GD = BE + 4, YI, YA, VR, DRAIN = VR + 3, XT, PR = XT + 2, UR, SR, YR, kBars };
 
 // Bounded wait in few instructions (there are many of them, and the roles' code has to stay in the instruction
 // cache): gives up after kPolls polls, or as soon as another thread has; the caller goes on with what is there and
@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float
 template <int N, int P, bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
 scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
-            const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap my, const Args k) {
+            const __grid_constant__ CUtensorMap mbq, const __grid_constant__ CUtensorMap mc,
+            const __grid_constant__ CUtensorMap my, const Args k) {
   using Lay = Layout<N, kOut>;
   constexpr int NH = 128 / P;                 // heads of this CTA
   constexpr int NB = N / 64;
@@ -283,6 +284,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::bars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::bars + kBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::bars + kBars * 8 + 8);
+  static_assert(kBars * 8 + 12 <= 256, "barriers");
   auto bar = [&](int i) { return sb + Lay::bars + 8u * i; };
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) tc::mbar_init(tc::smem_u32(&bars[i]), i == DRAIN ? (kOut ? 2 : 1) : i == YR ? 256 : i >= XT ? 128 : 1);
@@ -319,8 +321,16 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         for (int i = 0; i < NB; ++i) tma_load_2d(dst + i * kTile, m, bar(b), g * N + i * 64, row0 + c * L);
       };
       int bs = 0, cs = 0, vs = 0;             // loads issued
+      // With outputs there is room for one B tile: a quarter of the next one takes its place as soon as U and G have
+      // read that quarter, so that U does not wait for a whole tile.
+      auto load_q = [&](int qd, int c) {
+        tc::mbar_arrive_expect_tx(bar(BF + qd), NB * (kTile / 4));
+#pragma unroll 1
+        for (int i = 0; i < NB; ++i)
+          tma_load_2d(sb + Lay::b + i * kTile + qd * (kTile / 4), &mbq, bar(BF + qd), g * N + i * 64, row0 + c * L + qd * 32);
+      };
       auto load_b = [&] {
-        const int buf = kOut ? 0 : bs & 1;
+        const int buf = bs & 1;
         load_n(sb + Lay::b + buf * NB * kTile, &mb, BF + buf, bs);
         ++bs;
       };
@@ -332,28 +342,35 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       };
 #pragma unroll 1
       while (vs < nc && vs < 3) load_v();
+      if (kOut) {
 #pragma unroll 1
-      while (bs < nc && bs < (kOut ? 1 : 2)) load_b();
-      if (kOut) load_n(sb + Lay::c, &mc, CF, cs++);
+        for (; bs < 4; ++bs) load_q(bs, 0);
+        load_n(sb + Lay::c, &mc, CF, cs++);
+      } else {
+#pragma unroll 1
+        while (bs < nc && bs < 2) load_b();
+      }
 #pragma unroll 1
       for (int c = 0; c < nc && !*abort_flag; ++c) {
         if (kOut) {
-          wait(GD, c);                        // both have read B
-          wait(U1, c);
-        } else {
-          wait(BE + (c & 1), c >> 1);
-        }
-        if (bs < nc) load_b();
-        if (kOut) {
+          wait(GD, c);
+#pragma unroll 1
+          for (int qd = 0; qd < 4; ++qd) {
+            wait(BE + qd, c);
+            if (c + 1 < nc) load_q(qd, c + 1);
+          }
           wait(YI, c);
           if (cs < nc) load_n(sb + Lay::c, &mc, CF, cs++);
+        } else {
+          wait(BE + (c & 1), c >> 1);
+          if (bs < nc) load_b();
         }
         // the slot of chunk c - 1: U(c) was issued after its state, Yi(c) after its y
         if (c >= 1 && vs < nc) load_v();
       }
       // every load issued lands before the CTA can leave
       if (kOut) {
-        bounded_wait(bar(BF), (bs - 1) & 1, &never);
+        for (int qd = 0; qd < 4; ++qd) bounded_wait(bar(BF + qd), (cs - 1) & 1, &never);
         bounded_wait(bar(CF), (cs - 1) & 1, &never);
       } else {
         for (int i = max(0, bs - 2); i < bs; ++i) bounded_wait(bar(BF + (i & 1)), (i >> 1) & 1, &never);
@@ -399,11 +416,12 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       for (int c = 0; c < nc; ++c) {
         const int bbuf = kOut ? 0 : c & 1;
         const uint64_t dbt = tc::desc_adv(db0, bbuf * NB * kTile);
-        wait(BF + bbuf, kOut ? c : c >> 1);
+        if (!kOut) wait(BF + bbuf, c >> 1);
         if (c > 0) wait(UR, c - 1);
         // a quarter of the chunk's tokens: 2 steps of 16 for each of the three terms
 #pragma unroll 1
         for (int qd = 0; qd < 4; ++qd) {
+          if (kOut) wait(BF + qd, c);
           wait(XT + (qd & 1), 2 * c + (qd >> 1));
           tc::tc_fence_after();
           const uint64_t dw = tc::desc_adv(dxw, (qd & 1) * kSlot), dq = tc::desc_adv(dbt, qd * (kTile / 4));
@@ -412,6 +430,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
             mma_ss(tmem + TU, tc::desc_adv(dw, (i >> 1) * (kTile / 2) + (i & 1) * 2048), tc::desc_adv(dq, (i & 1) * 2048),
                    ID_U, qd + i > 0, leader);
           commit(bar(UQ + (qd & 1)), leader);
+          if (kOut) commit(bar(BE + qd), leader);
         }
         commit(bar(U1), leader);
         if (!kOut) commit(bar(BE + bbuf), leader);
@@ -429,7 +448,8 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       const uint64_t dx0 = tc::sdesc_sw128(sb + Lay::x, kTile, 1024);      // x, K = t
 #pragma unroll 1
       for (int c = 0; c < nc; ++c) {
-        wait(BF, c);
+#pragma unroll 1
+        for (int qd = 0; qd < 4; ++qd) wait(BF + qd, c);
         wait(CF, c);
         // G = C B^T, then Yi = C S
 #pragma unroll 1
@@ -499,7 +519,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         const int valid = min(L, sp.len - (ch0 + c) * L);
         if (valid < L) {     // rows behind the sequence reach no product: another sequence's, maybe NaN
           // (G may be reading B meanwhile: it yields columns s >= valid, which no row t < valid keeps)
-          wait(BF, c);
+          for (int i = 0; i < 4; ++i) wait(BF + i, c);
           zero_rows(sb + Lay::b, NB, valid, t);
         }
       }
@@ -710,8 +730,9 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
             zr[e] = *reinterpret_cast<const uint4*>(zp + 16 * i + 8 * e);
           }
         };
-        uint4 zr[2];
-        load_z(0, zr);
+        uint4 za[2], zb[2];                          // two pieces ahead, touched by nothing before their use
+        load_z(0, za);
+        load_z(1, zb);
         if (gated && y_on && c + 1 < nc && (ch0 + c + 1) * L + t < sp.len)     // the next chunk's into L2
           asm volatile("prefetch.global.L2 [%0];" ::"l"(zp + L * a.ldz));
         wait(XF + (c & 1), c >> 1);
@@ -719,15 +740,12 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         tc::tc_fence_after();
         const float e = vec_of(c)[VE + hs * 128 + t];
         const uint64_t e2 = tc::f2(e, e);
-#pragma unroll 1
-        for (int i = 0; i < 4 && y_on; ++i) {
+        auto piece = [&](int i, uint4 (&zr)[2]) {
           float yi[16], ya[16];
           tmem_ld16(tlane + TYI + 64 * half + 16 * i, yi);
           tmem_ld16(tlane + TYA + 64 * half + 16 * i, ya);
           const uint32_t at0 = xt + half * kTile + tc::sw128(t, 2 * i), at1 = xt + half * kTile + tc::sw128(t, 2 * i + 1);
           const uint4 xq[2] = {tc::ld_shared_v4(at0), tc::ld_shared_v4(at1)};
-          uint4 zn[2];
-          if (i < 3) load_z(i + 1, zn);
           tc::tmem_wait_ld();
           uint32_t o[2][4];
 #pragma unroll
@@ -756,8 +774,12 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
             to[0] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
             to[1] = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
           }
-          zr[0] = zn[0];
-          zr[1] = zn[1];
+          if (i < 2) load_z(i + 2, zr);
+        };
+#pragma unroll 1
+        for (int i = 0; i < 4 && y_on; i += 2) {
+          piece(i, za);
+          piece(i + 1, zb);
         }
         tc::tc_fence_before();
         tc::fence_proxy_async_smem();
@@ -789,14 +811,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   }();
   return fn;
 }
-// [rows, cols] bf16, rows ld values apart, boxes of 64 columns x 128 rows, 128-byte swizzle; rows
+// [rows, cols] bf16, rows ld values apart, boxes of 64 columns x box_rows, 128-byte swizzle; rows
 // past the end load as zeros and are not stored.
-inline bool make_map(CUtensorMap* m, const void* base, long rows, long cols, long ld) {
+inline bool make_map(CUtensorMap* m, const void* base, long rows, long cols, long ld, int box_rows = L) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)L}, estr[2] = {1, 1};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -835,9 +857,9 @@ int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
   const int segs = segments(a.nseq, a.max_len, a.H, a.G, P);
   float* vecs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + space(a.nseq, a.max_len, a.H, a.G, P, N).vecs);
   const Args k{a, static_cast<float*>(ws), vecs, chunks, (chunks + segs - 1) / segs, segs};
-  CUtensorMap mx, mb, mc, my;
+  CUtensorMap mx, mb, mbq, mc, my;
   if (!make_map(&mx, a.x, rows, (long)a.H * P, a.ldx) || !make_map(&mb, a.B, rows, (long)a.G * N, a.ldb) ||
-      !make_map(&mc, a.C, rows, (long)a.G * N, a.ldc) || !make_map(&my, a.y, rows, (long)a.H * P, (long)a.H * P))
+      !make_map(&mbq, a.B, rows, (long)a.G * N, a.ldb, L / 4) || !make_map(&mc, a.C, rows, (long)a.G * N, a.ldc) || !make_map(&my, a.y, rows, (long)a.H * P, (long)a.H * P))
     return GDN_ERR_CUDA;
   const dim3 grid((unsigned)columns(a.H, a.G, P), (unsigned)segs, (unsigned)a.nseq);
   decay_kernel<NH><<<dim3(grid.x, (unsigned)chunks, grid.z), 128 * NH, 0, st>>>(a, vecs);
@@ -846,13 +868,13 @@ int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
     auto first = scan_kernel<N, P, false>;
     if (cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, false>::alloc) != cudaSuccess)
       return GDN_ERR_CUDA;
-    first<<<dim3(grid.x, grid.y - 1, grid.z), kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mc, my, k);
+    first<<<dim3(grid.x, grid.y - 1, grid.z), kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mbq, mc, my, k);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   }
   auto kern = scan_kernel<N, P, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, true>::alloc) != cudaSuccess)
     return GDN_ERR_CUDA;
-  kern<<<grid, kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mc, my, k);
+  kern<<<grid, kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mbq, mc, my, k);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
