@@ -24,8 +24,7 @@
 // Roles: five warpgroups that run ahead of one another as far as the tiles and accumulators allow.
 //   warp 0 loads B, C and the chunks' decay vectors, warp 2 loads x tiles and stores y, warp 3 issues the MMAs of U in
 //     four quarters of 32 tokens, warp 1 those of G, Yi and Ya;
-//   warpgroup 1 forms X' (it reads x from global memory into registers, so that the x tile can hold y until
-//     that is stored);
+//   warpgroup 1 forms X';
 //   warpgroup 2 forms P and keeps the state in registers (a thread a row hp of S^T);
 //   warpgroups 3 and 4 form y, 64 columns each, in place of x in its tile, which leaves by a TMA store.
 // B and C, which the heads of a group share, come from L2.
@@ -72,11 +71,11 @@ constexpr uint32_t kVec = (2 * 128 * 5 + 16) * 4;
 constexpr int VU = 0, VW = 256, VE = 512, VP = 768, VT = 1280, VD = 1288;
 
 // Shared memory.  With the outputs: x tiles of two chunks, B, C, the state operand, two slots of X' (32 tokens
-// each), vectors, barriers.  Without: B of two chunks.
+// each), vectors, barriers.  Without: x and B of two chunks, X'.
 template <int N, bool kOut> struct Layout {
   static constexpr uint32_t NB = N / 64;
   static constexpr uint32_t x = 0;                                  // [2][2] tiles
-  static constexpr uint32_t b = kOut ? 4 * kTile : 0;               // [1 or 2][NB] tiles
+  static constexpr uint32_t b = 4 * kTile;                          // [1 or 2][NB] tiles
   static constexpr uint32_t c = b + (kOut ? 1 : 2) * NB * kTile;
   static constexpr uint32_t s = c + (kOut ? NB * kTile : 0);
   static constexpr uint32_t xw = s + (kOut ? NB * kTile : 0);       // [2 slots][3 terms][2] quarter tiles
@@ -88,7 +87,7 @@ template <int N, bool kOut> struct Layout {
 };
 
 // Barriers.  By TMA: XF (two x tiles), BF (B's four quarters; without outputs two buffers), CF, VR (three vector slots).  By MMA commits: UQ (the two X' slots read), U1 (U
-// complete), BE (the same parts of B read by U), GD (G), YI, YA.  By the
+// complete), BE (the same parts of B read by U; without outputs BX, x's two tiles read), GD (G), YI, YA.  By the
 // threads of the warpgroups: XT (two X' slots staged), PR (P), UR (U is in registers), SR (the state operand), YR (y in
 // its tile, Yi and Ya read).
 // A wait names a phase by its parity alone, so each one below stands where the phase after the awaited
@@ -102,7 +101,7 @@ __device__ __forceinline__ float log2_step(float v) {
   return r;
 }
 
-enum Bar { XF = 0, BF = 2, CF = BF + 4, UQ, U1 = UQ + 2, BE, GD = BE + 4, YI, YA, VR, DRAIN = VR + 3, XT, PR = XT + 2, UR, SR, YR, kBars };
+enum Bar { XF = 0, BF = 2, CF = BF + 4, UQ, U1 = UQ + 2, BE, GD = BE + 4, BX = BE + 2, YI = GD + 1, YA, VR, DRAIN = VR + 3, XT, PR = XT + 2, UR, SR, YR, kBars };
 
 // Bounded wait in few instructions (there are many of them, and the roles' code has to stay in the instruction
 // cache): gives up after kPolls polls, or as soon as another thread has; the caller goes on with what is there and
@@ -138,6 +137,11 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint3
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),
+               "r"(c1)
+               : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const void* map, uint32_t src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
@@ -292,7 +296,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     tc::fence_barrier_init();
   }
   if (warp == 1) tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmem);
-  if (kOut && NH == 2 && heads == 1) {        // the missing head's x tiles: zeros, never loaded
+  if (NH == 2 && heads == 1) {                // the missing head's x tiles: zeros, never loaded
     for (int i = tid; i < 2 * (int)kTile / 16; i += kThreads) {
       const int buf = i / ((int)kTile / 16), o = i % ((int)kTile / 16);
       tc::st_shared_v4(sb + Lay::x + (2 * buf + 1) * kTile + o * 16, 0, 0, 0, 0);
@@ -378,19 +382,23 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       for (int i = max(0, vs - 3); i < vs; ++i) bounded_wait(bar(VR + i % 3), (i / 3) & 1, &never);
     } else if (warp == 2 && lane == 0 && nc > 0) {
       // --------------------------------- x and y -----------------------------------------------
-      if constexpr (kOut) {
-        int xs = 0;
-        auto load_x = [&] {
-          const uint32_t dst = sb + Lay::x + (xs & 1) * 2 * kTile, b = bar(XF + (xs & 1));
-          tc::mbar_arrive_expect_tx(b, (NH == 2 && heads == 1 ? 1 : 2) * kTile);
-          tma_load_2d(dst, &mx, b, h0 * P, row0 + xs * L);
-          if (NH == 1 || heads == 2) tma_load_2d(dst + kTile, &mx, b, h0 * P + 64, row0 + xs * L);
-          ++xs;
-        };
+      int xs = 0;
+      auto load_x = [&] {
+        const uint32_t dst = sb + Lay::x + (xs & 1) * 2 * kTile, b = bar(XF + (xs & 1));
+        tc::mbar_arrive_expect_tx(b, (NH == 2 && heads == 1 ? 1 : 2) * kTile);
+        tma_load_2d(dst, &mx, b, h0 * P, row0 + xs * L);
+        if (NH == 1 || heads == 2) tma_load_2d(dst + kTile, &mx, b, h0 * P + 64, row0 + xs * L);
+        ++xs;
+      };
 #pragma unroll 1
-        while (xs < nc && xs < 2) load_x();
+      while (xs < nc && xs < 2) load_x();
 #pragma unroll 1
-        for (int c = 0; c < nc && !*abort_flag; ++c) {
+      for (int c = 0; c < nc && !*abort_flag; ++c) {
+        if (c + 2 < nc) {                     // into L2 while its tile is in use: the load then takes half the time
+          tma_prefetch_2d(&mx, h0 * P, row0 + (c + 2) * L);
+          if (NH == 1 || heads == 2) tma_prefetch_2d(&mx, h0 * P + 64, row0 + (c + 2) * L);
+        }
+        if (kOut) {
           wait(YR, c);
           if (sp.len - (ch0 + c) * L >= L) {
             const uint32_t src = sb + Lay::x + (c & 1) * 2 * kTile;
@@ -398,14 +406,14 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
             if (NH == 1 || heads == 2) tma_store_2d(&my, src + kTile, h0 * P + 64, row0 + c * L);
             tc::bulk_commit();
           }
-          if (xs < nc) {
-            tc::bulk_wait_read_all();
-            load_x();
-          }
+          if (xs < nc) tc::bulk_wait_read_all();
+        } else {
+          wait(BX + (c & 1), c >> 1);         // X' of the chunk is staged
         }
-        tc::bulk_wait_all();                  // every store has read its source before the CTA can leave
-        for (int i = max(0, xs - 2); i < xs; ++i) bounded_wait(bar(XF + (i & 1)), (i >> 1) & 1, &never);
+        if (xs < nc) load_x();
       }
+      if (kOut) tc::bulk_wait_all();          // every store has read its source before the CTA can leave
+      for (int i = max(0, xs - 2); i < xs; ++i) bounded_wait(bar(XF + (i & 1)), (i >> 1) & 1, &never);
     } else if (warp == 3 && nc > 0) {
       // ----------------------------------- MMAs of U -------------------------------------------
       const uint32_t leader = elect();
@@ -433,7 +441,10 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           if (kOut) commit(bar(BE + qd), leader);
         }
         commit(bar(U1), leader);
-        if (!kOut) commit(bar(BE + bbuf), leader);
+        if (!kOut) {
+          commit(bar(BE + bbuf), leader);
+          commit(bar(BX + bbuf), leader);
+        }
       }
       commit(bar(DRAIN), leader);
       bounded_wait(bar(DRAIN), 0, &never);
@@ -486,38 +497,17 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   } else if (wg == 1 || (!kOut && wg == 3)) {
     // ------------------------- X' (without outputs: every other quarter each) --------------------
     regs_dec<72>();
-    const bf16_t* xp = static_cast<const bf16_t*>(a.x) + (long)h0 * P;
     // this thread's four 16-byte pieces of a quarter: rows (t + 128 i) / 16, piece t % 16 of 16
     const int j = t & 7, tile = (t >> 3) & 1, r0 = t >> 4;
     constexpr int kStep = kOut ? 1 : 2;           // quarters from one of this warpgroup's to its next
-    const int q0 = wg == 1 ? 0 : 1;
-    uint4 xa[4], xb[4];                           // this quarter's pieces and the next one's: each is loaded a quarter
-    auto load_x = [&](int qq, uint4 (&xv)[4]) {   // ahead and touched by nothing before its use (a move would wait)
-      const int at = ch0 * L + qq * 32 + r0;
-      const bf16_t* p = xp + (sp.row0 + at) * a.ldx + tile * 64 + j * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        xv[i] = make_uint4(0, 0, 0, 0);
-        if (qq < 4 * nc && at + 8 * i < sp.len && (NH == 1 || tile < heads))
-          xv[i] = *reinterpret_cast<const uint4*>(p + (long)(8 * i) * a.ldx);
-      }
-    };
-    auto quarter = [&](int qq, uint4 (&xv)[4]) {
+#pragma unroll 1
+    for (int qq = wg == 1 ? 0 : 1; qq < 4 * nc; qq += kStep) {
       const int c = qq >> 2, qd = qq & 3, slot = qd & 1;
-      const float* vec = vec_of(c);
+      const int valid = min(L, sp.len - (ch0 + c) * L);
       if (qd < kStep) {
         wait(VR + c % 3, c / 3);
-        // the next chunk's rows into L2: the loads a quarter ahead then take no longer than a quarter
-        const int at = (ch0 + c + 1) * L + t;
-        if (c + 1 < nc && at < sp.len) {
-          const bf16_t* p = xp + (sp.row0 + at) * a.ldx;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-          if (NH == 1 || heads == 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64));
-        }
-      }
-      if (kOut && qd == 0) {
-        const int valid = min(L, sp.len - (ch0 + c) * L);
-        if (valid < L) {     // rows behind the sequence reach no product: another sequence's, maybe NaN
+        wait(XF + (c & 1), c >> 1);
+        if (kOut && valid < L) {   // rows behind the sequence reach no product: another sequence's, maybe NaN
           // (G may be reading B meanwhile: it yields columns s >= valid, which no row t < valid keeps)
           for (int i = 0; i < 4; ++i) wait(BF + i, c);
           zero_rows(sb + Lay::b, NB, valid, t);
@@ -525,13 +515,16 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       }
       if (qq >= 2) wait(UQ + slot, (qq >> 1) - 1);      // the slot is free again
       // three bf16 terms that add up to the fp32 product
+      const uint32_t from = sb + Lay::x + ((c & 1) * 2 + tile) * kTile + qd * (kTile / 4);
       const uint32_t dst = sb + Lay::xw + slot * kSlot + tile * (kTile / 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 8 * i;
-        const float w = vec[VW + (NH == 2 ? tile : 0) * 128 + qd * 32 + r];
+      const float* w_ = vec_of(c) + VW + (NH == 2 ? tile : 0) * 128 + qd * 32;
+#pragma unroll 2
+      for (int r = r0; r < 32; r += 8) {
+        uint4 xv = tc::ld_shared_v4(from + tc::sw128(r, j));
+        if (qd * 32 + r >= valid) xv = make_uint4(0, 0, 0, 0);
+        const float w = w_[r];
         const uint64_t ww = tc::f2(w, w);
-        const uint32_t in[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+        const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
         uint32_t o0[4], o1[4], o2[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -552,14 +545,6 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       }
       tc::fence_proxy_async_smem();
       tc::mbar_arrive(bar(XT + slot));
-      load_x(qq + 2 * kStep, xv);
-    };
-    load_x(q0, xa);
-    load_x(q0 + kStep, xb);
-#pragma unroll 1
-    for (int qq = q0; qq < 4 * nc; qq += 2 * kStep) {   // a chunk's quarters of this warpgroup are two or four
-      quarter(qq, xa);
-      quarter(qq + kStep, xb);
     }
   } else if (wg == 2) {
     // ----------------------------------- P and the state -----------------------------------------
