@@ -33,9 +33,10 @@
 // of 1000 instructions run by one warp, and what bounds this kernel is how fast the SM gets its instructions
 // (78 KB of code for all roles; every role that got shorter made the others faster).
 //
-// A sequence may be cut into segments that run side by side: a first launch (kOut = false) leaves
-// each segment's own final state and its total decay in the workspace, and the second starts every
-// segment from the states before it, combined in order (the result does not depend on timing).
+// A sequence's columns may be cut into segments that run side by side: a first launch (kOut = false) leaves each
+// segment's own final state and its total decay in the workspace, and the second starts every segment from the
+// states before it, combined in order (the result does not depend on timing).  That is done for the (sequence,
+// column) pairs that do not fill a wave of the SMs: 192 of them run as 148 whole ones and 44 in three segments.
 #pragma once
 
 #include <cuda.h>
@@ -57,10 +58,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
   ScanArgs a;
-  float* ws;                    // segment states, then segment decays (segments > 1)
-  const float* vecs;            // decay vectors: [nseq, columns, chunks] records of kVec bytes
+  float* ws;                    // [pairs cut][segments - 1] of a state [N][128] and two decays
+  const float* vecs;            // decay vectors: [pairs][chunks] records of kVec bytes
   int chunks;                   // chunks of the longest sequence
-  int seg_chunks, segments;     // chunks of a segment; segments of the longest sequence
+  int columns, whole;           // pair = sequence * columns + column; the first `whole` pairs are not cut
+  int seg_chunks, segments;     // the others: chunks of a segment, segments of the longest sequence
 };
 
 constexpr uint32_t kSlot = 6 * kTile / 4;      // X' of 32 tokens: three terms, two 64-column quarter tiles each
@@ -272,15 +274,21 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be uniform)
 
+  // this CTA's pair and segment: the whole pairs first, then the segments of each of the others
+  const int per = kOut ? k.segments : k.segments - 1;
+  const int cutb = (int)blockIdx.x - (kOut ? k.whole : 0);
+  const bool cut = cutb >= 0;
+  const int pair = cut ? k.whole + cutb / per : (int)blockIdx.x;
+  const int seg = cut ? cutb % per : 0;
+  const int seq = pair / k.columns, col = pair % k.columns;
   const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH;
-  const int g = blockIdx.x / pairs, pr = blockIdx.x % pairs;
+  const int g = col / pairs, pr = col % pairs;
   const int h0 = g * hpg + pr * NH;
   const int heads = min(NH, hpg - pr * NH);   // 1 where a group's last pair has one head only
-  const int seg = blockIdx.y, seq = blockIdx.z;
   const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
   const int chunks = (sp.len + L - 1) / L;
   const int ch0 = seg * k.seg_chunks;
-  const int nc = min(k.seg_chunks, chunks - ch0);
+  const int nc = cut ? min(k.seg_chunks, chunks - ch0) : chunks;
   const bool last = ch0 + nc >= chunks;       // this segment ends the sequence
   if (seg > 0 && nc <= 0) return;
   if (!kOut && (last || nc <= 0)) return;
@@ -338,7 +346,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         load_n(sb + Lay::b + buf * NB * kTile, &mb, BF + buf, bs);
         ++bs;
       };
-      const float* src = k.vecs + (((long)seq * gridDim.x + blockIdx.x) * k.chunks + ch0) * (kVec / 4);
+      const float* src = k.vecs + ((long)pair * k.chunks + ch0) * (kVec / 4);
       auto load_v = [&] {
         tc::mbar_arrive_expect_tx(bar(VR + vs % 3), kVec);
         tc::bulk_load(sb + Lay::vec + (vs % 3) * kVec, src + (long)vs * (kVec / 4), kVec, bar(VR + vs % 3));
@@ -555,8 +563,9 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     float S[N];                                      // row (sh, p) of S^T
     const long HNP = (long)a.H * N * P;
     const long srow = (long)(h0 + sh) * N * P + p;
-    float* wseg = k.ws + (long)seq * (k.segments - 1) * HNP + srow;
-    float* wdec = k.ws + (long)a.nseq * (k.segments - 1) * HNP + (long)seq * (k.segments - 1) * a.H + h0 + sh;
+    constexpr int kRec = N * 128 + 2;                // a segment's record
+    float* wseg = k.ws + (long)(pair - k.whole) * (k.segments - 1) * kRec + t;
+    const int sp_ = seg == 0 ? P : 128;              // distance of two state rows in what S starts from
     // the state before: S0, or those of the segments before, in order; 32 columns at a time
     const float* from0 = seg == 0 ? (a.S0 ? a.S0 + seq * HNP + srow : nullptr) : wseg;
     const int sources = !s_on || !from0 ? 0 : seg == 0 ? 1 : kOut ? seg : 0;
@@ -566,10 +575,10 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       for (int i = 0; i < 32; ++i) S[i0 + i] = 0.f;
 #pragma unroll 1
       for (int s = 0; s < sources; ++s) {
-        const float d = s > 0 ? wdec[(long)s * a.H] : 0.f;
-        const float* from = from0 + s * HNP + (long)i0 * P;
+        const float* from = from0 + (long)s * kRec;
+        const float d = s > 0 ? from[N * 128 + sh - t] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(d, S[i0 + i], from[(long)i * P]);
+        for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(d, S[i0 + i], from[(i0 + i) * sp_]);
       }
     }
     float seg_decay = 1.f;
@@ -685,8 +694,8 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) wseg[seg * HNP + (long)i * P] = S[i];
-        if (p == 0) wdec[(long)seg * a.H] = seg_decay;
+        for (int i = 0; i < N; ++i) wseg[(long)seg * kRec + i * 128] = S[i];
+        if (p == 0) wseg[(long)seg * kRec + N * 128 + sh - t] = seg_decay;
       }
     }
   } else {
@@ -814,24 +823,29 @@ inline int columns(int H, int G, int P) {       // CTAs of one sequence and segm
   const int nh = 128 / P;
   return G * ((H / G + nh - 1) / nh);
 }
-// Segments of the longest sequence, a rule on sizes alone (so that the workspace can be sized without
-// a device): one while the sequences and columns fill the SMs, else as many as still fit into one wave, none
-// shorter than four chunks (a segment costs the first launch and the combination, about two chunks' time).
-inline int segments(int nseq, int max_len, int H, int G, int P) {
-  const long ctas = (long)nseq * columns(H, G, P);
+// How the pairs are cut, a rule on sizes alone (so that the workspace can be sized without a device).  Of n pairs
+// floor(n / 148) full waves run whole; the rest r is cut into as many segments as fill one more wave, none shorter than
+// four chunks (a segment costs the first launch and the combination, about two chunks' time).  4 x 48 pairs of 16
+// chunks: 132 us whole in two waves, of which the second has 44 CTAs.  From five waves on nothing is cut.
+struct Cut {
+  int whole, segments;
+};
+inline Cut cut(int nseq, int max_len, int H, int G, int P) {
+  const long n = (long)nseq * columns(H, G, P), rest = n % 148;
   const int chunks = (max_len + L - 1) / L;
-  const long fit = 148 / (ctas > 0 ? ctas : 1);
-  const int s = (int)(fit < chunks / 4 ? fit : chunks / 4);
-  return s < 2 ? 1 : s;
+  if (rest == 0 || n > 148 * 5) return Cut{(int)n, 1};
+  const long s = 148 / rest < chunks / 4 ? 148 / rest : chunks / 4;
+  return s < 2 ? Cut{(int)n, 1} : Cut{(int)(n - rest), (int)s};
 }
 // The workspace: segment states and decays, then the decay vectors.
 struct Space {
   size_t vecs, bytes;
 };
 inline Space space(int nseq, int max_len, int H, int G, int P, int N) {
-  const size_t s = (size_t)segments(nseq, max_len, H, G, P) - 1, chunks = ((size_t)max_len + L - 1) / L;
-  const size_t states = ((size_t)nseq * s * H * ((size_t)N * P + 1) * sizeof(float) + 255) / 256 * 256;
-  return Space{states, states + (size_t)nseq * columns(H, G, P) * chunks * kVec};
+  const Cut c = cut(nseq, max_len, H, G, P);
+  const size_t pairs = (size_t)nseq * columns(H, G, P), chunks = ((size_t)max_len + L - 1) / L;
+  const size_t states = ((pairs - c.whole) * (c.segments - 1) * (N * 128 + 2) * sizeof(float) + 255) / 256 * 256;
+  return Space{states, states + pairs * chunks * kVec};
 }
 
 template <int N, int P>
@@ -839,27 +853,30 @@ int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
   constexpr int NH = 128 / P;
   const long rows = a.cu ? (long)a.T : (long)a.nseq * a.T;
   const int chunks = (a.max_len + L - 1) / L;
-  const int segs = segments(a.nseq, a.max_len, a.H, a.G, P);
+  const Cut ct = cut(a.nseq, a.max_len, a.H, a.G, P);
+  const int cols = columns(a.H, a.G, P);
+  const long pairs = (long)a.nseq * cols, rest = pairs - ct.whole;
+  if (pairs > 0x3fffffffL) return GDN_ERR_UNSUPPORTED;
   float* vecs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + space(a.nseq, a.max_len, a.H, a.G, P, N).vecs);
-  const Args k{a, static_cast<float*>(ws), vecs, chunks, (chunks + segs - 1) / segs, segs};
+  const Args k{a, static_cast<float*>(ws), vecs, chunks, cols, ct.whole, (chunks + ct.segments - 1) / ct.segments,
+               ct.segments};
   CUtensorMap mx, mb, mbq, mc, my;
   if (!make_map(&mx, a.x, rows, (long)a.H * P, a.ldx) || !make_map(&mb, a.B, rows, (long)a.G * N, a.ldb) ||
       !make_map(&mbq, a.B, rows, (long)a.G * N, a.ldb, L / 4) || !make_map(&mc, a.C, rows, (long)a.G * N, a.ldc) || !make_map(&my, a.y, rows, (long)a.H * P, (long)a.H * P))
     return GDN_ERR_CUDA;
-  const dim3 grid((unsigned)columns(a.H, a.G, P), (unsigned)segs, (unsigned)a.nseq);
-  decay_kernel<NH><<<dim3(grid.x, (unsigned)chunks, grid.z), 128 * NH, 0, st>>>(a, vecs);
+  decay_kernel<NH><<<dim3((unsigned)cols, (unsigned)chunks, (unsigned)a.nseq), 128 * NH, 0, st>>>(a, vecs);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
-  if (segs > 1) {
+  if (rest > 0) {
     auto first = scan_kernel<N, P, false>;
     if (cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, false>::alloc) != cudaSuccess)
       return GDN_ERR_CUDA;
-    first<<<dim3(grid.x, grid.y - 1, grid.z), kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mbq, mc, my, k);
+    first<<<(unsigned)(rest * (ct.segments - 1)), kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mbq, mc, my, k);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   }
   auto kern = scan_kernel<N, P, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, true>::alloc) != cudaSuccess)
     return GDN_ERR_CUDA;
-  kern<<<grid, kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mbq, mc, my, k);
+  kern<<<(unsigned)(ct.whole + rest * ct.segments), kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mbq, mc, my, k);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
