@@ -2,11 +2,13 @@
 //   D_t = softplus(dt_t + dt_bias)   S_t = exp(-D_t exp(A_log)) S_{t-1} + D_t B_t x_t^T
 //   y_t = (S_t^T C_t + D x_t) SiLU(z_t)
 //
-// A CTA owns PT = min(P, 32) columns of one (sequence, head): 128 threads as PT columns x NG
-// groups of N / NG state rows, the state in registers.  Tokens come in tiles of kTile through
-// shared memory (B and C as rows that a whole warp reads at one address); the NG partial read-outs
-// of a tile are added at its end.  Bound by the chain of tokens (3 N P operations each, issued by
-// four warps); it is the fp32 path and the one for shapes without a tensor-core kernel.
+// A CTA owns PT columns of one (sequence, head): 128 threads as PT columns x NG groups of N / NG state rows,
+// the state in registers.  Tokens come in tiles through shared memory (B and C as rows that a warp
+// reads at few addresses); the next tile is loaded into registers while this one is computed, and the NG
+// partial read-outs of a tile are added at its end.  Bound by the chain of tokens (3 N P operations each,
+// issued by four warps); it is the fp32 path and the one for shapes without a tensor-core kernel.  A tile of
+// 16 tokens that was loaded only when its turn came took 52 us for 2 x 333 tokens of 6 heads, most of it
+// the loads' latency.
 #pragma once
 
 #include "ssm_common.cuh"
@@ -15,14 +17,15 @@ namespace gdn {
 namespace ssm {
 
 constexpr int kSimtThreads = 128;
-constexpr int kTile = 16;
 
 template <int N, int P, typename T>
 __global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs a) {
   constexpr int PT = P < 32 ? P : 32;
   constexpr int NG = kSimtThreads / PT;
   constexpr int NR = N / NG;
-  static_assert(N % NG == 0, "state rows divide over the groups");
+  constexpr int kTile = N >= 128 ? 16 : 32;                     // tokens: 16 B and C values a thread at most
+  constexpr int kNB = (kTile * N + kSimtThreads - 1) / kSimtThreads, kNX = kTile * PT / kSimtThreads;
+  static_assert(N % NG == 0 && kTile * N % kSimtThreads == 0 && kTile * PT % kSimtThreads == 0, "tiles divide");
   const int nblk = P / PT;
   const int pb = blockIdx.x % nblk, h = blockIdx.x / nblk, seq = blockIdx.y;
   const int g = h / (a.H / a.G);
@@ -34,7 +37,7 @@ __global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs 
   __shared__ __align__(16) float sC[kTile][N];
   __shared__ float sx[kTile][PT];
   __shared__ float s_step[kTile], s_fade[kTile];
-  __shared__ float part[kTile][NG][PT + 1];
+  __shared__ float part[kTile][NG][PT];
 
   const T* __restrict__ x = static_cast<const T*>(a.x) + (long)h * P + p0;
   const T* __restrict__ dt = static_cast<const T*>(a.dt) + h;
@@ -51,26 +54,50 @@ __global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs 
 #pragma unroll
   for (int i = 0; i < NR; ++i) S[i] = a.S0 ? a.S0[sbase + (long)(ng * NR + i) * P] : 0.f;
 
+  T rb[kNB], rc[kNB], rx[kNX], rt;               // the next tile, as loaded
+  auto fetch = [&](int t0) {
+    const int nt = min(kTile, sp.len - t0);
+#pragma unroll
+    for (int k = 0; k < kNB; ++k) {
+      const int i = tid + k * kSimtThreads, t = i / N, n = i % N;
+      if (t < nt) {
+        const long r = sp.row0 + t0 + t;
+        rb[k] = Bm[r * a.ldb + n];
+        rc[k] = Cm[r * a.ldc + n];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kNX; ++k) {
+      const int i = tid + k * kSimtThreads, t = i / PT, p = i % PT;
+      if (t < nt) rx[k] = x[(sp.row0 + t0 + t) * a.ldx + p];
+    }
+    if (tid < nt) rt = dt[(sp.row0 + t0 + tid) * a.lddt];
+  };
+  fetch(0);
   for (int t0 = 0; t0 < sp.len; t0 += kTile) {
     const int nt = min(kTile, sp.len - t0);
-    __syncthreads();
-    for (int i = tid; i < nt * N; i += kSimtThreads) {
-      const int t = i / N, n = i % N;
-      const long r = sp.row0 + t0 + t;
-      sB[t][n] = to_f(Bm[r * a.ldb + n]);
-      sC[t][n] = to_f(Cm[r * a.ldc + n]);
+    __syncthreads();                             // the tile before has been read
+#pragma unroll
+    for (int k = 0; k < kNB; ++k) {
+      const int i = tid + k * kSimtThreads, t = i / N, n = i % N;
+      if (t < nt) {
+        sB[t][n] = to_f(rb[k]);
+        sC[t][n] = to_f(rc[k]);
+      }
     }
-    for (int i = tid; i < nt * PT; i += kSimtThreads) {
-      const int t = i / PT, p = i % PT;
-      sx[t][p] = to_f(x[(sp.row0 + t0 + t) * a.ldx + p]);
+#pragma unroll
+    for (int k = 0; k < kNX; ++k) {
+      const int i = tid + k * kSimtThreads, t = i / PT, p = i % PT;
+      if (t < nt) sx[t][p] = to_f(rx[k]);
     }
     if (tid < nt) {
-      const float step = softplus(to_f(dt[(sp.row0 + t0 + tid) * a.lddt]) + bias);
+      const float step = softplus(to_f(rt) + bias);
       s_step[tid] = step;
       s_fade[tid] = expf(step * rate);
     }
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
+    fetch(t0 + kTile);
+    auto token = [&](int t) {
       const float fade = s_fade[t], xd = sx[t][col] * s_step[t];
       float acc = 0.f;
 #pragma unroll
@@ -79,7 +106,13 @@ __global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs 
         acc = fmaf(S[i], sC[t][ng * NR + i], acc);
       }
       part[t][ng][col] = acc;
+    };
+    int t = 0;
+    for (; t + 4 <= nt; t += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) token(t + i);
     }
+    for (; t < nt; ++t) token(t);
     __syncthreads();
     for (int i = tid; i < nt * PT; i += kSimtThreads) {
       const int t = i / PT, p = i % PT;
