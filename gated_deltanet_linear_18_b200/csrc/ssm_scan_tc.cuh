@@ -33,6 +33,10 @@
 // of 1000 instructions run by one warp, and what bounds this kernel is how fast the SM gets its instructions
 // (78 KB of code for all roles; every role that got shorter made the others faster).
 //
+// One CTA an SM stays and takes one item after another (a sequence's columns, or a segment of them) from a counter;
+// the roles go on into the next item while others finish the last, so that a short sequence costs little more than its
+// chunks: a CTA for each item spent 14 us beside its chunks on filling and draining the pipeline.
+//
 // A sequence's columns may be cut into segments that run side by side: a first launch (kOut = false) leaves each
 // segment's own final state and its total decay in the workspace, and the second starts every segment from the
 // states before it, combined in order (the result does not depend on timing).  That is done for the (sequence,
@@ -58,11 +62,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
   ScanArgs a;
+  int* next;                    // the next item of each launch (set by the decay kernel)
   float* ws;                    // [pairs cut][segments - 1] of a state [N][128] and two decays
   const float* vecs;            // decay vectors: [pairs][chunks] records of kVec bytes
   int chunks;                   // chunks of the longest sequence
   int columns, whole;           // pair = sequence * columns + column; the first `whole` pairs are not cut
   int seg_chunks, segments;     // the others: chunks of a segment, segments of the longest sequence
+  int items;                    // of this launch
 };
 
 constexpr uint32_t kSlot = 6 * kTile / 4;      // X' of 32 tokens: three terms, two 64-column quarter tiles each
@@ -83,19 +89,20 @@ template <int N, bool kOut> struct Layout {
   static constexpr uint32_t xw = s + (kOut ? NB * kTile : 0);       // [2 slots][3 terms][2] quarter tiles
   static constexpr uint32_t vec = xw + 2 * kSlot;
   static constexpr uint32_t bars = vec + 3 * kVec;
-  static constexpr uint32_t bytes = bars + 256;
+  static constexpr uint32_t queue = bars + 320;                     // [4] items of 32 bytes
+  static constexpr uint32_t bytes = queue + 4 * 32;
   static constexpr uint32_t alloc = bytes + 1024;                   // the base is rounded up to 1024
   static_assert(alloc <= 232448, "shared memory of a CTA");
 };
 
-// Barriers.  By TMA: XF (two x tiles), BF (B's four quarters; without outputs two buffers), CF, VR (three vector slots).  By MMA commits: UQ (the two X' slots read), U1 (U
-// complete), BE (the same parts of B read by U; without outputs BX, x's two tiles read), GD (G), YI, YA.  By the
-// threads of the warpgroups: XT (two X' slots staged), PR (P), UR (U is in registers), SR (the state operand), YR (y in
-// its tile, Yi and Ya read).
+// Barriers.  By TMA: XF (two x tiles), BF (B's four quarters; without outputs two buffers), CF, VR (three vector
+// slots).  By warp 0: IQ (four items).  By MMA commits: UQ (the two X' slots read), U1 (U complete), BE (the same parts of
+// B read by U), BX (two: U complete and so x's tile read for X'), GD (G), YI, YA.  By the threads of the warpgroups: XT
+// (two X' slots staged), PR (P), UR (U is in registers), SR (the state operand), YR (two: y in its tile, Yi and Ya read).
 // A wait names a phase by its parity alone, so each one below stands where the phase after the awaited
 // one cannot have completed: what completes that needs something this waiter has yet to do.  For the same
-// reason only warp 3 waits for XT and only warpgroup 1 for VR; G, U and Y being complete implies the
-// vectors for the others.
+// reason YR and BX are kept by tile, only warp 3 waits for XT and only warpgroup 1 for VR; G, U and Y being complete
+// implies the vectors for the others.
 // log2 of a time step (0 gives -infinity: that token's weight is 0)
 __device__ __forceinline__ float log2_step(float v) {
   float r;
@@ -103,7 +110,10 @@ __device__ __forceinline__ float log2_step(float v) {
   return r;
 }
 
-enum Bar { XF = 0, BF = 2, CF = BF + 4, UQ, U1 = UQ + 2, BE, GD = BE + 4, BX = BE + 2, YI = GD + 1, YA, VR, DRAIN = VR + 3, XT, PR = XT + 2, UR, SR, YR, kBars };
+enum Bar {
+  XF = 0, BF = 2, CF = BF + 4, UQ, U1 = UQ + 2, BE, BX = BE + 4, GD = BX + 2, YI, YA, VR, IQ = VR + 3, DRAIN = IQ + 4,
+  XT, PR = XT + 2, UR, SR, YR, kBars = YR + 2
+};
 
 // Bounded wait in few instructions (there are many of them, and the roles' code has to stay in the instruction
 // cache): gives up after kPolls polls, or as soon as another thread has; the caller goes on with what is there and
@@ -209,14 +219,26 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 }
 
 // The decay vectors of every chunk: grid (columns, chunks, sequences), 128 threads for each of the column's heads, a
-// token a thread and a block of 32 tokens a warp.
+// token a thread and a block of 32 tokens a warp.  It also sets the item counters of the launches that follow, and hands
+// the state of a sequence without tokens on.
 template <int NH>
-__global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float* __restrict__ vecs) {
+__global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float* __restrict__ vecs, int* next, int2 first, int N) {
   const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH;
   const int g = blockIdx.x / pairs, pr = blockIdx.x % pairs;
   const int c = blockIdx.y, seq = blockIdx.z;
   const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
-  if (c * L >= sp.len) return;
+  if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x == 0) {
+    next[0] = first.x;
+    next[1] = first.y;
+  }
+  if (c * L >= sp.len) {
+    if (sp.len == 0 && c == 0 && a.S_T) {
+      constexpr int P = 128 / NH;
+      const long n = (long)min(NH, hpg - pr * NH) * N * P, at = ((long)seq * a.H + g * hpg + pr * NH) * N * P;
+      for (long i = threadIdx.x; i < n; i += 128 * NH) a.S_T[at + i] = a.S0 ? a.S0[at + i] : 0.f;
+    }
+    return;
+  }
   const int hs = threadIdx.x >> 7, t = threadIdx.x & 127, q = t >> 5, lane = t & 31;
   const int h = g * hpg + pr * NH + hs;
   const bool live = pr * NH + hs < hpg && c * L + t < sp.len;
@@ -273,190 +295,194 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   const uint32_t sb = tc::smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be uniform)
-
-  // this CTA's pair and segment: the whole pairs first, then the segments of each of the others
-  const int per = kOut ? k.segments : k.segments - 1;
-  const int cutb = (int)blockIdx.x - (kOut ? k.whole : 0);
-  const bool cut = cutb >= 0;
-  const int pair = cut ? k.whole + cutb / per : (int)blockIdx.x;
-  const int seg = cut ? cutb % per : 0;
-  const int seq = pair / k.columns, col = pair % k.columns;
-  const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH;
-  const int g = col / pairs, pr = col % pairs;
-  const int h0 = g * hpg + pr * NH;
-  const int heads = min(NH, hpg - pr * NH);   // 1 where a group's last pair has one head only
-  const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
-  const int chunks = (sp.len + L - 1) / L;
-  const int ch0 = seg * k.seg_chunks;
-  const int nc = cut ? min(k.seg_chunks, chunks - ch0) : chunks;
-  const bool last = ch0 + nc >= chunks;       // this segment ends the sequence
-  if (seg > 0 && nc <= 0) return;
-  if (!kOut && (last || nc <= 0)) return;
-
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::bars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::bars + kBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::bars + kBars * 8 + 8);
-  static_assert(kBars * 8 + 12 <= 256, "barriers");
+  static_assert(kBars * 8 + 12 <= 320, "barriers");
   auto bar = [&](int i) { return sb + Lay::bars + 8u * i; };
   if (tid == 0) {
-    for (int i = 0; i < kBars; ++i) tc::mbar_init(tc::smem_u32(&bars[i]), i == DRAIN ? (kOut ? 2 : 1) : i == YR ? 256 : i >= XT ? 128 : 1);
+    for (int i = 0; i < kBars; ++i) tc::mbar_init(tc::smem_u32(&bars[i]), i == DRAIN ? (kOut ? 2 : 1) : i >= YR ? 256 : i >= XT ? 128 : 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
   if (warp == 1) tc::tmem_alloc(tc::smem_u32(tmem_slot), kTmem);
-  if (NH == 2 && heads == 1) {                // the missing head's x tiles: zeros, never loaded
-    for (int i = tid; i < 2 * (int)kTile / 16; i += kThreads) {
-      const int buf = i / ((int)kTile / 16), o = i % ((int)kTile / 16);
-      tc::st_shared_v4(sb + Lay::x + (2 * buf + 1) * kTile + o * 16, 0, 0, 0, 0);
-    }
-    tc::fence_proxy_async_smem();
-  }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto wait = [&](int b, int phase) { bounded_wait(bar(b), (uint32_t)phase & 1u, abort_flag); };
-  const int row0 = (int)(sp.row0 + (long)ch0 * L);        // this segment's first row
   const int wg = warp >> 2, q = warp & 3;                 // warpgroup; lane quadrant
   const int t = tid & 127;                                // a token's (or hp's) row
   const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
-  auto vec_of = [&](int c) { return reinterpret_cast<float*>(smem + Lay::vec + (c % 3) * kVec); };
+  auto vec_of = [&](int cc) { return reinterpret_cast<float*>(smem + Lay::vec + (cc % 3) * kVec); };
+  // The n-th item of this CTA, for every role but warp 0, which writes it.  Four slots: warp 0 writes item n + 4 when
+  // the last chunk of item n + 3 is being loaded, and so after every role has done with chunks three before that.
+  struct Item {
+    int nc, row0, rows, h0, heads, seg, g, seq, pair;     // chunks (0: no more); first row, tokens from it to the end
+  };
+  auto item = [&](int n) {
+    wait(IQ + (n & 3), n >> 2);
+    const int4* r = reinterpret_cast<const int4*>(smem + Lay::queue + (n & 3) * 32);
+    const int4 u = r[0], v = r[1];
+    return Item{*abort_flag ? 0 : u.x, u.y, u.z, u.w, v.x & 255, v.x >> 8, v.y, v.z, v.w};
+  };
+  // In every role cc counts this CTA's chunks over all items (phases and buffers go by it), c those of the item.
 
   if (wg == 0) {
     regs_dec<56>();          // 56 + 72 + 192 + 2 x 80: the registers of five threads at launch (96 each)
     volatile int never = 0;
-    if (warp == 0 && lane == 0 && nc > 0) {
-      // ------------------------------- B, C and the decay vectors ------------------------------
-      auto load_n = [&](uint32_t dst, const CUtensorMap* m, int b, int c) {
+    if (warp == 0 && lane == 0) {
+      // --------------------- items, B, C and the decay vectors -----------------------------------
+      const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH, per = kOut ? k.segments : k.segments - 1;
+      auto load_n = [&](uint32_t dst, const CUtensorMap* m, int b, int col, int row) {
         tc::mbar_arrive_expect_tx(bar(b), NB * kTile);
 #pragma unroll 1
-        for (int i = 0; i < NB; ++i) tma_load_2d(dst + i * kTile, m, bar(b), g * N + i * 64, row0 + c * L);
+        for (int i = 0; i < NB; ++i) tma_load_2d(dst + i * kTile, m, bar(b), col + i * 64, row);
       };
-      int bs = 0, cs = 0, vs = 0;             // loads issued
-      // With outputs there is room for one B tile: a quarter of the next one takes its place as soon as U and G have
-      // read that quarter, so that U does not wait for a whole tile.
-      auto load_q = [&](int qd, int c) {
-        tc::mbar_arrive_expect_tx(bar(BF + qd), NB * (kTile / 4));
+      int cc = 0, n = 0;
 #pragma unroll 1
-        for (int i = 0; i < NB; ++i)
-          tma_load_2d(sb + Lay::b + i * kTile + qd * (kTile / 4), &mbq, bar(BF + qd), g * N + i * 64, row0 + c * L + qd * 32);
-      };
-      auto load_b = [&] {
-        const int buf = bs & 1;
-        load_n(sb + Lay::b + buf * NB * kTile, &mb, BF + buf, bs);
-        ++bs;
-      };
-      const float* src = k.vecs + ((long)pair * k.chunks + ch0) * (kVec / 4);
-      auto load_v = [&] {
-        tc::mbar_arrive_expect_tx(bar(VR + vs % 3), kVec);
-        tc::bulk_load(sb + Lay::vec + (vs % 3) * kVec, src + (long)vs * (kVec / 4), kVec, bar(VR + vs % 3));
-        ++vs;
-      };
+      for (int id = blockIdx.x; id < k.items && !*abort_flag; id = atomicAdd(k.next + (kOut ? 1 : 0), 1)) {
+        // the whole pairs first, then the segments of each of the others
+        const int cutb = id - (kOut ? k.whole : 0);
+        const bool cut = cutb >= 0;
+        const int pair = cut ? k.whole + cutb / per : id, seg = cut ? cutb % per : 0;
+        const int seq = pair / k.columns, col = pair % k.columns;
+        const int g = col / pairs, pr = col % pairs;
+        const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
+        const int ch0 = seg * k.seg_chunks, rows = sp.len - ch0 * L, chunks = (rows + L - 1) / L;
+        const int nc = cut ? min(k.seg_chunks, chunks) : chunks;
+        if (rows <= 0 || (!kOut && nc == chunks)) continue;       // (without outputs: nor a sequence's last segment)
+        const int row0 = (int)(sp.row0 + (long)ch0 * L);
+        int4* r = reinterpret_cast<int4*>(smem + Lay::queue + (n & 3) * 32);
+        r[0] = make_int4(nc, row0, rows, g * hpg + pr * NH);
+        r[1] = make_int4(min(NH, hpg - pr * NH) | seg << 8, g, seq, pair);
+        tc::mbar_arrive(bar(IQ + (n & 3)));
+        ++n;
+        const float* src = k.vecs + ((long)pair * k.chunks + ch0) * (kVec / 4);
 #pragma unroll 1
-      while (vs < nc && vs < 3) load_v();
-      if (kOut) {
+        for (int c = 0; c < nc && !*abort_flag; ++c, ++cc) {
+          // the vectors' slot held chunk cc - 3's, which every role is through with: this thread has seen (with outputs) Yi
+          // of cc - 2, issued after y of cc - 3, or U of cc - 3 or later, issued after the state of the chunk before it
+          if (!kOut && cc >= 2) wait(BE + (cc & 1), (cc >> 1) - 1);
+          tc::mbar_arrive_expect_tx(bar(VR + cc % 3), kVec);
+          tc::bulk_load(sb + Lay::vec + (cc % 3) * kVec, src + (long)c * (kVec / 4), kVec, bar(VR + cc % 3));
+          const int row = row0 + c * L;
+          if constexpr (kOut) {
+            // There is room for one B tile: a quarter of the next one takes its place as soon as U and G have read that
+            // quarter, so that U does not wait for a whole tile.
+            if (cc > 0) wait(GD, cc - 1);
 #pragma unroll 1
-        for (; bs < 4; ++bs) load_q(bs, 0);
-        load_n(sb + Lay::c, &mc, CF, cs++);
-      } else {
+            for (int qd = 0; qd < 4; ++qd) {
+              if (cc > 0) wait(BE + qd, cc - 1);
+              tc::mbar_arrive_expect_tx(bar(BF + qd), NB * (kTile / 4));
 #pragma unroll 1
-        while (bs < nc && bs < 2) load_b();
-      }
-#pragma unroll 1
-      for (int c = 0; c < nc && !*abort_flag; ++c) {
-        if (kOut) {
-          wait(GD, c);
-#pragma unroll 1
-          for (int qd = 0; qd < 4; ++qd) {
-            wait(BE + qd, c);
-            if (c + 1 < nc) load_q(qd, c + 1);
+              for (int i = 0; i < NB; ++i)
+                tma_load_2d(sb + Lay::b + i * kTile + qd * (kTile / 4), &mbq, bar(BF + qd), g * N + i * 64, row + qd * 32);
+            }
+            if (cc > 0) wait(YI, cc - 1);
+            load_n(sb + Lay::c, &mc, CF, g * N, row);
+          } else {
+            load_n(sb + Lay::b + (cc & 1) * NB * kTile, &mb, BF + (cc & 1), g * N, row);
           }
-          wait(YI, c);
-          if (cs < nc) load_n(sb + Lay::c, &mc, CF, cs++);
-        } else {
-          wait(BE + (c & 1), c >> 1);
-          if (bs < nc) load_b();
         }
-        // the slot of chunk c - 1: U(c) was issued after its state, Yi(c) after its y
-        if (c >= 1 && vs < nc) load_v();
       }
+      reinterpret_cast<int4*>(smem + Lay::queue + (n & 3) * 32)[0] = make_int4(0, 0, 0, 0);
+      tc::mbar_arrive(bar(IQ + (n & 3)));
       // every load issued lands before the CTA can leave
-      if (kOut) {
-        for (int qd = 0; qd < 4; ++qd) bounded_wait(bar(BF + qd), (cs - 1) & 1, &never);
-        bounded_wait(bar(CF), (cs - 1) & 1, &never);
-      } else {
-        for (int i = max(0, bs - 2); i < bs; ++i) bounded_wait(bar(BF + (i & 1)), (i >> 1) & 1, &never);
+      if (cc > 0) {
+        if (kOut) {
+          for (int qd = 0; qd < 4; ++qd) bounded_wait(bar(BF + qd), (cc - 1) & 1, &never);
+          bounded_wait(bar(CF), (cc - 1) & 1, &never);
+        } else {
+          for (int i = max(0, cc - 2); i < cc; ++i) bounded_wait(bar(BF + (i & 1)), (i >> 1) & 1, &never);
+        }
+        for (int i = max(0, cc - 3); i < cc; ++i) bounded_wait(bar(VR + i % 3), (i / 3) & 1, &never);
       }
-      for (int i = max(0, vs - 3); i < vs; ++i) bounded_wait(bar(VR + i % 3), (i / 3) & 1, &never);
-    } else if (warp == 2 && lane == 0 && nc > 0) {
+    } else if (warp == 2 && lane == 0) {
       // --------------------------------- x and y -----------------------------------------------
-      int xs = 0;
-      auto load_x = [&] {
-        const uint32_t dst = sb + Lay::x + (xs & 1) * 2 * kTile, b = bar(XF + (xs & 1));
-        tc::mbar_arrive_expect_tx(b, (NH == 2 && heads == 1 ? 1 : 2) * kTile);
-        tma_load_2d(dst, &mx, b, h0 * P, row0 + xs * L);
-        if (NH == 1 || heads == 2) tma_load_2d(dst + kTile, &mx, b, h0 * P + 64, row0 + xs * L);
-        ++xs;
+      int cc = 0;
+      int4 y1 = make_int4(0, 0, 0, 0), y2 = y1;           // y of the last two chunks: (row, column, second tile, whole)
+      auto store_y = [&](int4 y, int at) {
+        wait(YR + (at & 1), at >> 1);
+        if (y.w) {
+          const uint32_t src = sb + Lay::x + (at & 1) * 2 * kTile;
+          tma_store_2d(&my, src, y.y, y.x);
+          if (y.z) tma_store_2d(&my, src + kTile, y.y + 64, y.x);
+          tc::bulk_commit();
+        }
       };
 #pragma unroll 1
-      while (xs < nc && xs < 2) load_x();
+      for (int n = 0;; ++n) {
+        const Item it = item(n);
+        if (it.nc == 0) break;
 #pragma unroll 1
-      for (int c = 0; c < nc && !*abort_flag; ++c) {
-        if (c + 2 < nc) {                     // into L2 while its tile is in use: the load then takes half the time
-          tma_prefetch_2d(&mx, h0 * P, row0 + (c + 2) * L);
-          if (NH == 1 || heads == 2) tma_prefetch_2d(&mx, h0 * P + 64, row0 + (c + 2) * L);
-        }
-        if (kOut) {
-          wait(YR, c);
-          if (sp.len - (ch0 + c) * L >= L) {
-            const uint32_t src = sb + Lay::x + (c & 1) * 2 * kTile;
-            tma_store_2d(&my, src, h0 * P, row0 + c * L);
-            if (NH == 1 || heads == 2) tma_store_2d(&my, src + kTile, h0 * P + 64, row0 + c * L);
-            tc::bulk_commit();
+        for (int c = 0; c < it.nc && !*abort_flag; ++c, ++cc) {
+          const int row = it.row0 + c * L, col = it.h0 * P;
+          // a missing second head's tile gets the first one's x: it reaches no row or column that is kept
+          const int col1 = NH == 1 || it.heads == 2 ? col + 64 : col;
+          if (cc >= 2) {                      // into L2 while the tile is in use: the load then takes half the time
+            tma_prefetch_2d(&mx, col, row);
+            tma_prefetch_2d(&mx, col1, row);
+            if constexpr (kOut) {
+              store_y(y2, cc - 2);
+              tc::bulk_wait_read_all();
+            } else {
+              wait(BX + (cc & 1), (cc >> 1) - 1);         // X' of chunk cc - 2 is staged
+            }
           }
-          if (xs < nc) tc::bulk_wait_read_all();
-        } else {
-          wait(BX + (c & 1), c >> 1);         // X' of the chunk is staged
+          const uint32_t dst = sb + Lay::x + (cc & 1) * 2 * kTile, b = bar(XF + (cc & 1));
+          tc::mbar_arrive_expect_tx(b, 2 * kTile);
+          tma_load_2d(dst, &mx, b, col, row);
+          tma_load_2d(dst + kTile, &mx, b, col1, row);
+          y2 = y1;
+          y1 = make_int4(row, col, NH == 1 || it.heads == 2, it.rows - c * L >= L);
         }
-        if (xs < nc) load_x();
       }
-      if (kOut) tc::bulk_wait_all();          // every store has read its source before the CTA can leave
-      for (int i = max(0, xs - 2); i < xs; ++i) bounded_wait(bar(XF + (i & 1)), (i >> 1) & 1, &never);
-    } else if (warp == 3 && nc > 0) {
+      if (kOut) {
+        if (cc >= 2) store_y(y2, cc - 2);
+        if (cc >= 1) store_y(y1, cc - 1);
+        tc::bulk_wait_all();                  // every store has read its source before the CTA can leave
+      }
+      for (int i = max(0, cc - 2); i < cc; ++i) bounded_wait(bar(XF + (i & 1)), (i >> 1) & 1, &never);
+    } else if (warp == 3) {
       // ----------------------------------- MMAs of U -------------------------------------------
       const uint32_t leader = elect();
       constexpr uint32_t ID_U = tc::idesc_bf16(128, N, true, true);
       const uint64_t dxw = tc::sdesc_sw128(sb + Lay::xw, kTile / 4, 1024);                      // X', K = t
       const uint64_t db0 = tc::sdesc_sw128(sb + Lay::b, kTile, 1024);                           // B, K = t
+      int cc = 0;
 #pragma unroll 1
-      for (int c = 0; c < nc; ++c) {
-        const int bbuf = kOut ? 0 : c & 1;
-        const uint64_t dbt = tc::desc_adv(db0, bbuf * NB * kTile);
-        if (!kOut) wait(BF + bbuf, c >> 1);
-        if (c > 0) wait(UR, c - 1);
-        // a quarter of the chunk's tokens: 2 steps of 16 for each of the three terms
+      for (int n = 0;; ++n) {
+        const int nc = item(n).nc;
+        if (nc == 0) break;
 #pragma unroll 1
-        for (int qd = 0; qd < 4; ++qd) {
-          if (kOut) wait(BF + qd, c);
-          wait(XT + (qd & 1), 2 * c + (qd >> 1));
-          tc::tc_fence_after();
-          const uint64_t dw = tc::desc_adv(dxw, (qd & 1) * kSlot), dq = tc::desc_adv(dbt, qd * (kTile / 4));
+        for (int c = 0; c < nc; ++c, ++cc) {
+          const int bbuf = kOut ? 0 : cc & 1;
+          const uint64_t dbt = tc::desc_adv(db0, bbuf * NB * kTile);
+          if (!kOut) wait(BF + bbuf, cc >> 1);
+          if (cc > 0) wait(UR, cc - 1);
+          // a quarter of the chunk's tokens: 2 steps of 16 for each of the three terms
+#pragma unroll 1
+          for (int qd = 0; qd < 4; ++qd) {
+            if (kOut) wait(BF + qd, cc);
+            wait(XT + (qd & 1), 2 * cc + (qd >> 1));
+            tc::tc_fence_after();
+            const uint64_t dw = tc::desc_adv(dxw, (qd & 1) * kSlot), dq = tc::desc_adv(dbt, qd * (kTile / 4));
 #pragma unroll
-          for (int i = 0; i < 6; ++i)
-            mma_ss(tmem + TU, tc::desc_adv(dw, (i >> 1) * (kTile / 2) + (i & 1) * 2048), tc::desc_adv(dq, (i & 1) * 2048),
-                   ID_U, qd + i > 0, leader);
-          commit(bar(UQ + (qd & 1)), leader);
-          if (kOut) commit(bar(BE + qd), leader);
-        }
-        commit(bar(U1), leader);
-        if (!kOut) {
-          commit(bar(BE + bbuf), leader);
-          commit(bar(BX + bbuf), leader);
+            for (int i = 0; i < 6; ++i)
+              mma_ss(tmem + TU, tc::desc_adv(dw, (i >> 1) * (kTile / 2) + (i & 1) * 2048), tc::desc_adv(dq, (i & 1) * 2048),
+                     ID_U, qd + i > 0, leader);
+            commit(bar(UQ + (qd & 1)), leader);
+            if (kOut) commit(bar(BE + qd), leader);
+          }
+          commit(bar(U1), leader);
+          commit(bar(BX + (cc & 1)), leader);
+          if (!kOut) commit(bar(BE + bbuf), leader);
         }
       }
       commit(bar(DRAIN), leader);
       bounded_wait(bar(DRAIN), 0, &never);
-    } else if (kOut && warp == 1 && nc > 0) {
+    } else if (kOut && warp == 1) {
       // ----------------------------------- MMAs of G, Yi, Ya -----------------------------------
       const uint32_t leader = elect();
       constexpr uint32_t ID_G = tc::idesc_bf16(128, 128, false, false);
@@ -465,39 +491,45 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       const uint64_t db = tc::sdesc_sw128(sb + Lay::b, 16, 1024);          // B, K = n
       const uint64_t ds = tc::sdesc_sw128(sb + Lay::s, 16, 1024);          // S^T, K = n
       const uint64_t dx0 = tc::sdesc_sw128(sb + Lay::x, kTile, 1024);      // x, K = t
+      int cc = 0;
 #pragma unroll 1
-      for (int c = 0; c < nc; ++c) {
+      for (int n = 0;; ++n) {
+        const int nc = item(n).nc;
+        if (nc == 0) break;
 #pragma unroll 1
-        for (int qd = 0; qd < 4; ++qd) wait(BF + qd, c);
-        wait(CF, c);
-        // G = C B^T, then Yi = C S
+        for (int c = 0; c < nc; ++c, ++cc) {
 #pragma unroll 1
-        for (int w = 0; w < 2; ++w) {
-          if (w) {
-            wait(SR, c);
-            if (c > 0) wait(YR, c - 1);
+          for (int qd = 0; qd < 4; ++qd) wait(BF + qd, cc);
+          wait(CF, cc);
+          // G = C B^T, then Yi = C S
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            if (w) {
+              wait(SR, cc);
+              if (cc > 0) wait(YR + ((cc - 1) & 1), (cc - 1) >> 1);
+            }
+            tc::tc_fence_after();
+            const uint64_t dn = w ? ds : db;
+#pragma unroll 1
+            for (int m = 0; m < NB; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_ss(tmem + (w ? TYI : TG), tc::desc_adv(dc, m * kTile + i * 32), tc::desc_adv(dn, m * kTile + i * 32),
+                       ID_G, m + i > 0, leader);
+            commit(bar(w ? YI : GD), leader);
           }
+          wait(XF + (cc & 1), cc >> 1);
+          wait(PR, cc);
           tc::tc_fence_after();
-          const uint64_t dn = w ? ds : db;
+          const uint64_t dx = tc::desc_adv(dx0, (cc & 1) * 2 * kTile);
 #pragma unroll 1
-          for (int n = 0; n < NB; ++n)
+          for (int hs = 0; hs < NH; ++hs)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_ss(tmem + (w ? TYI : TG), tc::desc_adv(dc, n * kTile + i * 32), tc::desc_adv(dn, n * kTile + i * 32), ID_G,
-                     n + i > 0, leader);
-          commit(bar(w ? YI : GD), leader);
+            for (int i = 0; i < 8; ++i)
+              mma_ts(tmem + TYA + hs * 64, tmem + TG + 32 * (i >> 1) + 16 * hs + 8 * (i & 1),
+                     tc::desc_adv(dx, hs * kTile + i * 2048), ID_YA, i > 0, leader);
+          commit(bar(YA), leader);
         }
-        wait(XF + (c & 1), c >> 1);
-        wait(PR, c);
-        tc::tc_fence_after();
-        const uint64_t dx = tc::desc_adv(dx0, (c & 1) * 2 * kTile);
-#pragma unroll 1
-        for (int hs = 0; hs < NH; ++hs)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            mma_ts(tmem + TYA + hs * 64, tmem + TG + 32 * (i >> 1) + 16 * hs + 8 * (i & 1),
-                   tc::desc_adv(dx, hs * kTile + i * 2048), ID_YA, i > 0, leader);
-        commit(bar(YA), leader);
       }
       commit(bar(DRAIN), leader);
       bounded_wait(bar(DRAIN), 0, &never);
@@ -508,80 +540,67 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     // this thread's four 16-byte pieces of a quarter: rows (t + 128 i) / 16, piece t % 16 of 16
     const int j = t & 7, tile = (t >> 3) & 1, r0 = t >> 4;
     constexpr int kStep = kOut ? 1 : 2;           // quarters from one of this warpgroup's to its next
+    int cc = 0;
 #pragma unroll 1
-    for (int qq = wg == 1 ? 0 : 1; qq < 4 * nc; qq += kStep) {
-      const int c = qq >> 2, qd = qq & 3, slot = qd & 1;
-      const int valid = min(L, sp.len - (ch0 + c) * L);
-      if (qd < kStep) {
-        wait(VR + c % 3, c / 3);
-        wait(XF + (c & 1), c >> 1);
+    for (int n = 0;; ++n) {
+      const Item it = item(n);
+      if (it.nc == 0) break;
+#pragma unroll 1
+      for (int c = 0; c < it.nc; ++c, ++cc) {
+        const int valid = min(L, it.rows - c * L);
+        wait(VR + cc % 3, cc / 3);
+        wait(XF + (cc & 1), cc >> 1);
         if (kOut && valid < L) {   // rows behind the sequence reach no product: another sequence's, maybe NaN
           // (G may be reading B meanwhile: it yields columns s >= valid, which no row t < valid keeps)
-          for (int i = 0; i < 4; ++i) wait(BF + i, c);
+          for (int i = 0; i < 4; ++i) wait(BF + i, cc);
           zero_rows(sb + Lay::b, NB, valid, t);
         }
-      }
-      if (qq >= 2) wait(UQ + slot, (qq >> 1) - 1);      // the slot is free again
-      // three bf16 terms that add up to the fp32 product
-      const uint32_t from = sb + Lay::x + ((c & 1) * 2 + tile) * kTile + qd * (kTile / 4);
-      const uint32_t dst = sb + Lay::xw + slot * kSlot + tile * (kTile / 4);
-      const float* w_ = vec_of(c) + VW + (NH == 2 ? tile : 0) * 128 + qd * 32;
+#pragma unroll 1
+        for (int qd = wg == 1 ? 0 : 1; qd < 4; qd += kStep) {
+          const int slot = qd & 1, use = 2 * cc + (qd >> 1);
+          if (use > 0) wait(UQ + slot, use - 1);          // the slot is free again
+          // three bf16 terms that add up to the fp32 product
+          const uint32_t from = sb + Lay::x + ((cc & 1) * 2 + tile) * kTile + qd * (kTile / 4);
+          const uint32_t dst = sb + Lay::xw + slot * kSlot + tile * (kTile / 4);
+          const float* w_ = vec_of(cc) + VW + (NH == 2 ? tile : 0) * 128 + qd * 32;
 #pragma unroll 2
-      for (int r = r0; r < 32; r += 8) {
-        uint4 xv = tc::ld_shared_v4(from + tc::sw128(r, j));
-        if (qd * 32 + r >= valid) xv = make_uint4(0, 0, 0, 0);
-        const float w = w_[r];
-        const uint64_t ww = tc::f2(w, w);
-        const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
-        uint32_t o0[4], o1[4], o2[4];
+          for (int r = r0; r < 32; r += 8) {
+            uint4 xv = tc::ld_shared_v4(from + tc::sw128(r, j));
+            if (qd * 32 + r >= valid) xv = make_uint4(0, 0, 0, 0);
+            const float w = w_[r];
+            const uint64_t ww = tc::f2(w, w);
+            const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
+            uint32_t o0[4], o1[4], o2[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint64_t f = tc::mul2(tc::f2(tc::bf16lo(in[e]), tc::bf16hi(in[e])), ww);
-          float f0, f1;
-          tc::f2_get(f, f0, f1);
-          o0[e] = tc::pack_bf16(f0, f1);
-          const uint64_t g2 = tc::sub2(f, tc::f2(tc::bf16lo(o0[e]), tc::bf16hi(o0[e])));
-          tc::f2_get(g2, f0, f1);
-          o1[e] = tc::pack_bf16(f0, f1);
-          tc::f2_get(tc::sub2(g2, tc::f2(tc::bf16lo(o1[e]), tc::bf16hi(o1[e]))), f0, f1);
-          o2[e] = tc::pack_bf16(f0, f1);
+            for (int e = 0; e < 4; ++e) {
+              const uint64_t f = tc::mul2(tc::f2(tc::bf16lo(in[e]), tc::bf16hi(in[e])), ww);
+              float f0, f1;
+              tc::f2_get(f, f0, f1);
+              o0[e] = tc::pack_bf16(f0, f1);
+              const uint64_t g2 = tc::sub2(f, tc::f2(tc::bf16lo(o0[e]), tc::bf16hi(o0[e])));
+              tc::f2_get(g2, f0, f1);
+              o1[e] = tc::pack_bf16(f0, f1);
+              tc::f2_get(tc::sub2(g2, tc::f2(tc::bf16lo(o1[e]), tc::bf16hi(o1[e]))), f0, f1);
+              o2[e] = tc::pack_bf16(f0, f1);
+            }
+            const uint32_t at = dst + tc::sw128(r, j);
+            tc::st_shared_v4(at, o0[0], o0[1], o0[2], o0[3]);
+            tc::st_shared_v4(at + kTile / 2, o1[0], o1[1], o1[2], o1[3]);
+            tc::st_shared_v4(at + kTile, o2[0], o2[1], o2[2], o2[3]);
+          }
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(bar(XT + slot));
         }
-        const uint32_t at = dst + tc::sw128(r, j);
-        tc::st_shared_v4(at, o0[0], o0[1], o0[2], o0[3]);
-        tc::st_shared_v4(at + kTile / 2, o1[0], o1[1], o1[2], o1[3]);
-        tc::st_shared_v4(at + kTile, o2[0], o2[1], o2[2], o2[3]);
       }
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(bar(XT + slot));
     }
   } else if (wg == 2) {
     // ----------------------------------- P and the state -----------------------------------------
     regs_inc<192>();
     const int sh = NH == 2 ? (t >> 6) : 0;           // the head of state row t
     const int p = NH == 2 ? (t & 63) : t;
-    const bool s_on = sh < heads;
-    float S[N];                                      // row (sh, p) of S^T
     const long HNP = (long)a.H * N * P;
-    const long srow = (long)(h0 + sh) * N * P + p;
     constexpr int kRec = N * 128 + 2;                // a segment's record
-    float* wseg = k.ws + (long)(pair - k.whole) * (k.segments - 1) * kRec + t;
-    const int sp_ = seg == 0 ? P : 128;              // distance of two state rows in what S starts from
-    // the state before: S0, or those of the segments before, in order; 32 columns at a time
-    const float* from0 = seg == 0 ? (a.S0 ? a.S0 + seq * HNP + srow : nullptr) : wseg;
-    const int sources = !s_on || !from0 ? 0 : seg == 0 ? 1 : kOut ? seg : 0;
-#pragma unroll
-    for (int i0 = 0; i0 < N; i0 += 32) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) S[i0 + i] = 0.f;
-#pragma unroll 1
-      for (int s = 0; s < sources; ++s) {
-        const float* from = from0 + (long)s * kRec;
-        const float d = s > 0 ? from[N * 128 + sh - t] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(d, S[i0 + i], from[(i0 + i) * sp_]);
-      }
-    }
-    float seg_decay = 1.f;
+    float S[N];                                      // row (sh, p) of S^T
     auto publish_state = [&] {                       // the copy that the next chunk's Yi reads
 #pragma unroll
       for (int i = 0; i < N / 8; ++i)
@@ -591,111 +610,148 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       tc::fence_proxy_async_smem();
       tc::mbar_arrive(bar(SR));
     };
-    if (kOut && nc > 0) publish_state();
-    for (int c = 0; c < nc; ++c) {
-      const float* vec = vec_of(c);
-      if constexpr (kOut) {
-        // ---- P from G
-        wait(GD, c);
-        tc::tc_fence_after();
-        float mid[NH], mine[NH];
-#pragma unroll
-        for (int hs = 0; hs < NH; ++hs) mid[hs] = mine[hs] = vec[VP + hs * 128 + t];
+    int cc = 0;
 #pragma unroll 1
-        for (int b = 3; b >= 0; --b) {
-          const uint32_t at = tlane + TG + 32 * b;
-          if (b > q) {                               // after every token of these rows
-            uint32_t o[16];
+    for (int n = 0;; ++n) {
+      const Item it = item(n);
+      if (it.nc == 0) break;
+      const bool s_on = sh < it.heads;
+      const long srow = (long)it.seq * HNP + (long)(it.h0 + sh) * N * P + p;
+      float* wseg = k.ws + (long)(it.pair - k.whole) * (k.segments - 1) * kRec + t;
+      // the state before: S0, or those of the segments before, in order.  S0's loads are not waited for here: P of the
+      // item's first chunk comes before the first use of S
+      const float* from0 = it.seg == 0 ? (a.S0 ? a.S0 + srow : nullptr) : wseg;
+      const int step = it.seg == 0 ? P : 128;        // distance of two state rows there
+      const bool some = s_on && from0 != nullptr && (kOut || it.seg == 0);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = 0;
-            tmem_st16(at, o);
-            if (NH == 2) tmem_st16(at + 16, o);
-            continue;
-          }
-          float G[32];
-          tc::tmem_ld32(at, G);
-          tc::tmem_wait_ld();
+      for (int i = 0; i < N; ++i) S[i] = 0.f;
+      if (some) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) S[i] = from0[i * step];
+      }
+      if (kOut && some && it.seg > 1) {
+#pragma unroll
+        for (int i0 = 0; i0 < N; i0 += 32) {         // 32 columns at a time: the rest of S is in registers
 #pragma unroll 1
-          for (int hs = 0; hs < NH; ++hs) {
-            uint32_t o[16];
-            if (b < q) {
-              const float r = tc::ex2(hs ? mid[NH - 1] : mid[0]);
-              const uint64_t rr = tc::f2(r, r);
-              const float4* u4 = reinterpret_cast<const float4*>(vec + VU + hs * 128 + 32 * b);
+          for (int s = 1; s < it.seg; ++s) {
+            const float* from = wseg + (long)s * kRec;
+            const float d = from[N * 128 + sh - t];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 u = u4[i];
-                float f0, f1;
-                tc::f2_get(tc::mul2(tc::f2(G[4 * i], G[4 * i + 1]), tc::mul2(tc::f2(u.x, u.y), rr)), f0, f1);
-                o[2 * i] = tc::pack_bf16(f0, f1);
-                tc::f2_get(tc::mul2(tc::f2(G[4 * i + 2], G[4 * i + 3]), tc::mul2(tc::f2(u.z, u.w), rr)), f0, f1);
-                o[2 * i + 1] = tc::pack_bf16(f0, f1);
-              }
-            } else {
-              const float m = hs ? mine[NH - 1] : mine[0];
-              const float4* p4 = reinterpret_cast<const float4*>(vec + VP + 256 + hs * 128 + 32 * b);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 v = p4[i];              // prefix - log2 D of columns 4 i .. 4 i + 3
-                const float f0 = 4 * i <= lane ? G[4 * i] * tc::ex2(m - v.x) : 0.f;
-                const float f1 = 4 * i + 1 <= lane ? G[4 * i + 1] * tc::ex2(m - v.y) : 0.f;
-                const float f2 = 4 * i + 2 <= lane ? G[4 * i + 2] * tc::ex2(m - v.z) : 0.f;
-                const float f3 = 4 * i + 3 <= lane ? G[4 * i + 3] * tc::ex2(m - v.w) : 0.f;
-                o[2 * i] = tc::pack_bf16(f0, f1);
-                o[2 * i + 1] = tc::pack_bf16(f2, f3);
-              }
-            }
-            tmem_st16(at + 16 * hs, o);
-          }
-          if (b < q) {                               // the blocks between: whole
-#pragma unroll
-            for (int hs = 0; hs < NH; ++hs) mid[hs] += vec[VT + hs * 4 + b];
+            for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(d, S[i0 + i], from[(i0 + i) * 128]);
           }
         }
-        tc::tmem_wait_st();
-        const int valid = min(L, sp.len - (ch0 + c) * L);
-        if (valid < L) {                             // nor do x's rows behind the sequence reach Ya
-          wait(XF + (c & 1), c >> 1);
-          zero_rows(sb + Lay::x + (c & 1) * 2 * kTile, 2, valid, t);
-          tc::fence_proxy_async_smem();
+      }
+      float seg_decay = 1.f;
+#pragma unroll 1
+      for (int c = 0; c < it.nc; ++c, ++cc) {
+        const float* vec = vec_of(cc);
+        if constexpr (kOut) {
+          // ---- P from G
+          wait(GD, cc);
+          tc::tc_fence_after();
+          float mid[NH], mine[NH];
+#pragma unroll
+          for (int hs = 0; hs < NH; ++hs) mid[hs] = mine[hs] = vec[VP + hs * 128 + t];
+#pragma unroll 1
+          for (int b = 3; b >= 0; --b) {
+            const uint32_t at = tlane + TG + 32 * b;
+            if (b > q) {                             // after every token of these rows
+              uint32_t o[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = 0;
+              tmem_st16(at, o);
+              if (NH == 2) tmem_st16(at + 16, o);
+              continue;
+            }
+            float G[32];
+            tc::tmem_ld32(at, G);
+            tc::tmem_wait_ld();
+#pragma unroll 1
+            for (int hs = 0; hs < NH; ++hs) {
+              uint32_t o[16];
+              if (b < q) {
+                const float r = tc::ex2(hs ? mid[NH - 1] : mid[0]);
+                const uint64_t rr = tc::f2(r, r);
+                const float4* u4 = reinterpret_cast<const float4*>(vec + VU + hs * 128 + 32 * b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 u = u4[i];
+                  float f0, f1;
+                  tc::f2_get(tc::mul2(tc::f2(G[4 * i], G[4 * i + 1]), tc::mul2(tc::f2(u.x, u.y), rr)), f0, f1);
+                  o[2 * i] = tc::pack_bf16(f0, f1);
+                  tc::f2_get(tc::mul2(tc::f2(G[4 * i + 2], G[4 * i + 3]), tc::mul2(tc::f2(u.z, u.w), rr)), f0, f1);
+                  o[2 * i + 1] = tc::pack_bf16(f0, f1);
+                }
+              } else {
+                const float m = hs ? mine[NH - 1] : mine[0];
+                const float4* p4 = reinterpret_cast<const float4*>(vec + VP + 256 + hs * 128 + 32 * b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 v = p4[i];            // prefix - log2 D of columns 4 i .. 4 i + 3
+                  const float f0 = 4 * i <= lane ? G[4 * i] * tc::ex2(m - v.x) : 0.f;
+                  const float f1 = 4 * i + 1 <= lane ? G[4 * i + 1] * tc::ex2(m - v.y) : 0.f;
+                  const float f2 = 4 * i + 2 <= lane ? G[4 * i + 2] * tc::ex2(m - v.z) : 0.f;
+                  const float f3 = 4 * i + 3 <= lane ? G[4 * i + 3] * tc::ex2(m - v.w) : 0.f;
+                  o[2 * i] = tc::pack_bf16(f0, f1);
+                  o[2 * i + 1] = tc::pack_bf16(f2, f3);
+                }
+              }
+              tmem_st16(at + 16 * hs, o);
+            }
+            if (b < q) {                             // the blocks between: whole
+#pragma unroll
+              for (int hs = 0; hs < NH; ++hs) mid[hs] += vec[VT + hs * 4 + b];
+            }
+          }
+          tc::tmem_wait_st();
+          const int valid = min(L, it.rows - c * L);
+          if (valid < L) {                           // nor do x's rows behind the sequence reach Ya
+            wait(XF + (cc & 1), cc >> 1);
+            zero_rows(sb + Lay::x + (cc & 1) * 2 * kTile, 2, valid, t);
+            tc::fence_proxy_async_smem();
+          }
+          tc::tc_fence_before();
+          tc::mbar_arrive(bar(PR));
+          if (c == 0) {
+            if (cc > 0) wait(YI, cc - 1);            // Yi has read the item before's copy
+            publish_state();
+          }
+        }
+        // ---- S' = exp(c_L) S + U
+        wait(U1, cc);
+        tc::tc_fence_after();
+        const float d = vec[VD + sh];
+        seg_decay *= d;
+        const uint64_t dd = tc::f2(d, d);
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {
+          float U[32];
+          tc::tmem_ld32(tlane + TU + 32 * i, U);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            tc::f2_get(tc::fma2(dd, tc::f2(S[32 * i + e], S[32 * i + e + 1]), tc::f2(U[e], U[e + 1])), S[32 * i + e],
+                       S[32 * i + e + 1]);
         }
         tc::tc_fence_before();
-        tc::mbar_arrive(bar(PR));
-      }
-      // ---- S' = exp(c_L) S + U
-      wait(U1, c);
-      tc::tc_fence_after();
-      const float d = vec[VD + sh];
-      seg_decay *= d;
-      const uint64_t dd = tc::f2(d, d);
-#pragma unroll
-      for (int i = 0; i < N / 32; ++i) {
-        float U[32];
-        tc::tmem_ld32(tlane + TU + 32 * i, U);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          tc::f2_get(tc::fma2(dd, tc::f2(S[32 * i + e], S[32 * i + e + 1]), tc::f2(U[e], U[e + 1])), S[32 * i + e],
-                     S[32 * i + e + 1]);
-      }
-      tc::tc_fence_before();
-      tc::mbar_arrive(bar(UR));
-      if (kOut && c + 1 < nc) {
-        wait(YI, c);                                 // Yi has read the copy before
-        publish_state();
-      }
-    }
-    // ---- the state after this segment
-    if (s_on) {
-      if constexpr (kOut) {
-        if (last && a.S_T) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) a.S_T[seq * HNP + srow + (long)i * P] = S[i];
+        tc::mbar_arrive(bar(UR));
+        if (kOut && c + 1 < it.nc) {
+          wait(YI, cc);                              // Yi has read the copy before
+          publish_state();
         }
-      } else {
+      }
+      // ---- the state after this item
+      if (s_on) {
+        if constexpr (kOut) {
+          if (it.rows <= it.nc * L && a.S_T) {       // it ends its sequence
 #pragma unroll
-        for (int i = 0; i < N; ++i) wseg[(long)seg * kRec + i * 128] = S[i];
-        if (p == 0) wseg[(long)seg * kRec + N * 128 + sh - t] = seg_decay;
+            for (int i = 0; i < N; ++i) a.S_T[srow + (long)i * P] = S[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) wseg[(long)it.seg * kRec + i * 128] = S[i];
+          if (p == 0) wseg[(long)it.seg * kRec + N * 128 + sh - t] = seg_decay;
+        }
       }
     }
   } else {
@@ -704,80 +760,89 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     if constexpr (kOut) {
       const int half = wg - 3;                       // this warpgroup's 64 columns
       const int hs = NH == 2 ? half : 0;             // their head
-      const bool y_on = hs < heads;
-      const float skip = a.D && y_on ? a.D[h0 + hs] : 0.f;
-      const uint64_t skip2 = tc::f2(skip, skip);
       const bool gated = a.z != nullptr;
-      for (int c = 0; c < nc; ++c) {
-        const int valid = min(L, sp.len - (ch0 + c) * L);
-        const long row = (long)row0 + c * L + t;
-        const uint32_t xt = sb + Lay::x + (c & 1) * 2 * kTile;
-        const bf16_t* zp = gated ? static_cast<const bf16_t*>(a.z) + row * a.ldz + (long)h0 * P + 64 * half : nullptr;
-        bf16_t* yp = static_cast<bf16_t*>(a.y) + row * ((long)a.H * P) + (long)h0 * P + 64 * half;
-        // the gate's values of 16 columns (piece i of this warpgroup's four)
-        auto load_z = [&](int i, uint4 (&zr)[2]) {
-          const bool on = gated && t < valid && y_on;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            zr[e] = make_uint4(0, 0, 0, 0);
-            if (!on) continue;
-            zr[e] = *reinterpret_cast<const uint4*>(zp + 16 * i + 8 * e);
-          }
-        };
-        uint4 za[2], zb[2];                          // two pieces ahead, touched by nothing before their use
-        load_z(0, za);
-        load_z(1, zb);
-        if (gated && y_on && c + 1 < nc && (ch0 + c + 1) * L + t < sp.len)     // the next chunk's into L2
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(zp + L * a.ldz));
-        wait(XF + (c & 1), c >> 1);
-        wait(YA, c);
-        tc::tc_fence_after();
-        const float e = vec_of(c)[VE + hs * 128 + t];
-        const uint64_t e2 = tc::f2(e, e);
-        auto piece = [&](int i, uint4 (&zr)[2]) {
-          float yi[16], ya[16];
-          tmem_ld16(tlane + TYI + 64 * half + 16 * i, yi);
-          tmem_ld16(tlane + TYA + 64 * half + 16 * i, ya);
-          const uint32_t at0 = xt + half * kTile + tc::sw128(t, 2 * i), at1 = xt + half * kTile + tc::sw128(t, 2 * i + 1);
-          const uint4 xq[2] = {tc::ld_shared_v4(at0), tc::ld_shared_v4(at1)};
-          tc::tmem_wait_ld();
-          uint32_t o[2][4];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const uint32_t xi[4] = {xq[m].x, xq[m].y, xq[m].z, xq[m].w};
-            const uint32_t zi[4] = {zr[m].x, zr[m].y, zr[m].z, zr[m].w};
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const int col = 8 * m + 2 * f;
-              uint64_t y2 = tc::fma2(skip2, tc::f2(tc::bf16lo(xi[f]), tc::bf16hi(xi[f])), tc::f2(ya[col], ya[col + 1]));
-              y2 = tc::fma2(e2, tc::f2(yi[col], yi[col + 1]), y2);
-              if (gated) {
-                const float z0 = tc::bf16lo(zi[f]), z1 = tc::bf16hi(zi[f]);
-                y2 = tc::mul2(y2, tc::mul2(tc::f2(z0, z1), tc::f2(sigmoid(z0), sigmoid(z1))));
-              }
-              float f0, f1;
-              tc::f2_get(y2, f0, f1);
-              o[m][f] = tc::pack_bf16(f0, f1);
-            }
-          }
-          if (valid == L) {
-            tc::st_shared_v4(at0, o[0][0], o[0][1], o[0][2], o[0][3]);
-            tc::st_shared_v4(at1, o[1][0], o[1][1], o[1][2], o[1][3]);
-          } else if (t < valid) {
-            uint4* to = reinterpret_cast<uint4*>(yp + 16 * i);
-            to[0] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-            to[1] = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-          }
-          if (i < 2) load_z(i + 2, zr);
-        };
+      int cc = 0;
 #pragma unroll 1
-        for (int i = 0; i < 4 && y_on; i += 2) {
-          piece(i, za);
-          piece(i + 1, zb);
+      for (int n = 0;; ++n) {
+        const Item it = item(n);
+        if (it.nc == 0) break;
+        const bool y_on = hs < it.heads;
+        const float skip = a.D && y_on ? a.D[it.h0 + hs] : 0.f;
+        const uint64_t skip2 = tc::f2(skip, skip);
+        const long col = (long)it.h0 * P + 64 * half;
+#pragma unroll 1
+        for (int c = 0; c < it.nc; ++c, ++cc) {
+          const int valid = min(L, it.rows - c * L);
+          const long row = (long)it.row0 + c * L + t;
+          const uint32_t xt = sb + Lay::x + (cc & 1) * 2 * kTile;
+          const bf16_t* zp = gated ? static_cast<const bf16_t*>(a.z) + row * a.ldz + col : nullptr;
+          bf16_t* yp = static_cast<bf16_t*>(a.y) + row * ((long)a.H * P) + col;
+          // the gate's values of 16 columns (piece i of this warpgroup's four)
+          auto load_z = [&](int i, uint4 (&zr)[2]) {
+            const bool on = gated && t < valid && y_on;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              zr[e] = make_uint4(0, 0, 0, 0);
+              if (!on) continue;
+              zr[e] = *reinterpret_cast<const uint4*>(zp + 16 * i + 8 * e);
+            }
+          };
+          uint4 za[2], zb[2];                        // two pieces ahead, touched by nothing before their use
+          load_z(0, za);
+          load_z(1, zb);
+          if (gated && y_on && (c + 1) * L + t < it.rows && c + 1 < it.nc)     // the next chunk's into L2
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(zp + L * a.ldz));
+          wait(XF + (cc & 1), cc >> 1);
+          wait(BX + (cc & 1), cc >> 1);              // warpgroup 1 has read x's tile: y may take its place
+          wait(YA, cc);
+          tc::tc_fence_after();
+          const float e = vec_of(cc)[VE + hs * 128 + t];
+          const uint64_t e2 = tc::f2(e, e);
+          auto piece = [&](int i, uint4 (&zr)[2]) {
+            float yi[16], ya[16];
+            tmem_ld16(tlane + TYI + 64 * half + 16 * i, yi);
+            tmem_ld16(tlane + TYA + 64 * half + 16 * i, ya);
+            const uint32_t at0 = xt + half * kTile + tc::sw128(t, 2 * i), at1 = xt + half * kTile + tc::sw128(t, 2 * i + 1);
+            const uint4 xq[2] = {tc::ld_shared_v4(at0), tc::ld_shared_v4(at1)};
+            tc::tmem_wait_ld();
+            uint32_t o[2][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const uint32_t xi[4] = {xq[m].x, xq[m].y, xq[m].z, xq[m].w};
+              const uint32_t zi[4] = {zr[m].x, zr[m].y, zr[m].z, zr[m].w};
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                const int at = 8 * m + 2 * f;
+                uint64_t y2 = tc::fma2(skip2, tc::f2(tc::bf16lo(xi[f]), tc::bf16hi(xi[f])), tc::f2(ya[at], ya[at + 1]));
+                y2 = tc::fma2(e2, tc::f2(yi[at], yi[at + 1]), y2);
+                if (gated) {
+                  const float z0 = tc::bf16lo(zi[f]), z1 = tc::bf16hi(zi[f]);
+                  y2 = tc::mul2(y2, tc::mul2(tc::f2(z0, z1), tc::f2(sigmoid(z0), sigmoid(z1))));
+                }
+                float f0, f1;
+                tc::f2_get(y2, f0, f1);
+                o[m][f] = tc::pack_bf16(f0, f1);
+              }
+            }
+            if (valid == L) {
+              tc::st_shared_v4(at0, o[0][0], o[0][1], o[0][2], o[0][3]);
+              tc::st_shared_v4(at1, o[1][0], o[1][1], o[1][2], o[1][3]);
+            } else if (t < valid) {
+              uint4* to = reinterpret_cast<uint4*>(yp + 16 * i);
+              to[0] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
+              to[1] = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
+            }
+            if (i < 2) load_z(i + 2, zr);
+          };
+#pragma unroll 1
+          for (int i = 0; i < 4 && y_on; i += 2) {
+            piece(i, za);
+            piece(i + 1, zb);
+          }
+          tc::tc_fence_before();
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(bar(YR + (cc & 1)));
         }
-        tc::tc_fence_before();
-        tc::fence_proxy_async_smem();
-        tc::mbar_arrive(bar(YR));
       }
     }
   }
@@ -837,7 +902,7 @@ inline Cut cut(int nseq, int max_len, int H, int G, int P) {
   const long s = 148 / rest < chunks / 4 ? 148 / rest : chunks / 4;
   return s < 2 ? Cut{(int)n, 1} : Cut{(int)(n - rest), (int)s};
 }
-// The workspace: segment states and decays, then the decay vectors.
+// The workspace: the item counters (256 bytes), segment states and decays, the decay vectors.
 struct Space {
   size_t vecs, bytes;
 };
@@ -845,7 +910,7 @@ inline Space space(int nseq, int max_len, int H, int G, int P, int N) {
   const Cut c = cut(nseq, max_len, H, G, P);
   const size_t pairs = (size_t)nseq * columns(H, G, P), chunks = ((size_t)max_len + L - 1) / L;
   const size_t states = ((pairs - c.whole) * (c.segments - 1) * (N * 128 + 2) * sizeof(float) + 255) / 256 * 256;
-  return Space{states, states + pairs * chunks * kVec};
+  return Space{256 + states, 256 + states + pairs * chunks * kVec};
 }
 
 template <int N, int P>
@@ -856,27 +921,32 @@ int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
   const Cut ct = cut(a.nseq, a.max_len, a.H, a.G, P);
   const int cols = columns(a.H, a.G, P);
   const long pairs = (long)a.nseq * cols, rest = pairs - ct.whole;
-  if (pairs > 0x3fffffffL) return GDN_ERR_UNSUPPORTED;
   float* vecs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + space(a.nseq, a.max_len, a.H, a.G, P, N).vecs);
-  const Args k{a, static_cast<float*>(ws), vecs, chunks, cols, ct.whole, (chunks + ct.segments - 1) / ct.segments,
-               ct.segments};
+  int* next = static_cast<int*>(ws);
+  Args k{a, next, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256), vecs, chunks, cols, ct.whole,
+         (chunks + ct.segments - 1) / ct.segments, ct.segments, 0};
+  const long cut_items = rest * (ct.segments - 1), items = ct.whole + rest * ct.segments;
+  if (items > 0x3fffffffL) return GDN_ERR_UNSUPPORTED;
+  const int2 ctas = make_int2((int)(cut_items < 148 ? cut_items : 148), (int)(items < 148 ? items : 148));
   CUtensorMap mx, mb, mbq, mc, my;
   if (!make_map(&mx, a.x, rows, (long)a.H * P, a.ldx) || !make_map(&mb, a.B, rows, (long)a.G * N, a.ldb) ||
       !make_map(&mbq, a.B, rows, (long)a.G * N, a.ldb, L / 4) || !make_map(&mc, a.C, rows, (long)a.G * N, a.ldc) || !make_map(&my, a.y, rows, (long)a.H * P, (long)a.H * P))
     return GDN_ERR_CUDA;
-  decay_kernel<NH><<<dim3((unsigned)cols, (unsigned)chunks, (unsigned)a.nseq), 128 * NH, 0, st>>>(a, vecs);
+  decay_kernel<NH><<<dim3((unsigned)cols, (unsigned)chunks, (unsigned)a.nseq), 128 * NH, 0, st>>>(a, vecs, next, ctas, N);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (rest > 0) {
     auto first = scan_kernel<N, P, false>;
     if (cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, false>::alloc) != cudaSuccess)
       return GDN_ERR_CUDA;
-    first<<<(unsigned)(rest * (ct.segments - 1)), kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mbq, mc, my, k);
+    k.items = (int)cut_items;
+    first<<<(unsigned)ctas.x, kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mbq, mc, my, k);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   }
   auto kern = scan_kernel<N, P, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, true>::alloc) != cudaSuccess)
     return GDN_ERR_CUDA;
-  kern<<<(unsigned)(ct.whole + rest * ct.segments), kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mbq, mc, my, k);
+  k.items = (int)items;
+  kern<<<(unsigned)ctas.y, kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mbq, mc, my, k);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
