@@ -218,64 +218,93 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The decay vectors of every chunk: grid (columns, chunks, sequences), 128 threads for each of the column's heads, a
-// token a thread and a block of 32 tokens a warp.  It also sets the item counters of the launches that follow, and hands
-// the state of a sequence without tokens on.
+// The decay vectors of every chunk: grid (blocks of kDecayCols columns, chunks, sequences), 128 threads for each of a
+// column's heads, a token a thread and a block of 32 tokens a warp.  The columns of a block share the sectors of a
+// token's dt row, all loaded before the first is used.  It also sets the item counters of the launches that follow, and
+// hands the state of a sequence without tokens on.
+constexpr int kDecayCols = 8;
 template <int NH>
-__global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float* __restrict__ vecs, int* next, int2 first, int N) {
+__global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float* __restrict__ vecs, int* next, int2 first, int N,
+                                                         int cols) {
   const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH;
-  const int g = blockIdx.x / pairs, pr = blockIdx.x % pairs;
   const int c = blockIdx.y, seq = blockIdx.z;
   const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
+  const int hs = threadIdx.x >> 7, t = threadIdx.x & 127, q = t >> 5, lane = t & 31;
   if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x == 0) {
     next[0] = first.x;
     next[1] = first.y;
   }
+  const int col0 = blockIdx.x * kDecayCols, ncol = min(kDecayCols, cols - col0);
+  // head of this thread in column col0 + i, or -1
+  auto head = [&](int i) {
+    const int g = (col0 + i) / pairs, in = ((col0 + i) % pairs) * NH + hs;
+    return i < ncol && in < hpg ? g * hpg + in : -1;
+  };
   if (c * L >= sp.len) {
     if (sp.len == 0 && c == 0 && a.S_T) {
-      constexpr int P = 128 / NH;
-      const long n = (long)min(NH, hpg - pr * NH) * N * P, at = ((long)seq * a.H + g * hpg + pr * NH) * N * P;
-      for (long i = threadIdx.x; i < n; i += 128 * NH) a.S_T[at + i] = a.S0 ? a.S0[at + i] : 0.f;
+      for (int i = 0; i < ncol; ++i) {
+        const int h = head(i);
+        if (h < 0) continue;
+        const int n = N * (128 / NH);
+        const long at = ((long)seq * a.H + h) * n;
+        for (int j = t; j < n; j += 128) a.S_T[at + j] = a.S0 ? a.S0[at + j] : 0.f;
+      }
     }
     return;
   }
-  const int hs = threadIdx.x >> 7, t = threadIdx.x & 127, q = t >> 5, lane = t & 31;
-  const int h = g * hpg + pr * NH + hs;
-  const bool live = pr * NH + hs < hpg && c * L + t < sp.len;
-  float* vec = vecs + (((long)seq * gridDim.x + blockIdx.x) * gridDim.y + c) * (kVec / 4);
-  __shared__ float4 tot[NH];
-  float step = 0.f, pre = 0.f;
-  if (live) {
-    const float raw = __bfloat162float(static_cast<const bf16_t*>(a.dt)[(sp.row0 + c * L + t) * a.lddt + h]);
-    step = softplus(raw + (a.dt_bias ? a.dt_bias[h] : 0.f));
-    pre = step * (-expf(a.A_log[h]) * kLog2e);
+  const bool row_on = c * L + t < sp.len;
+  const bf16_t* dt = static_cast<const bf16_t*>(a.dt) + (sp.row0 + c * L + t) * a.lddt;
+  bf16_t raw[kDecayCols];
+#pragma unroll
+  for (int i = 0; i < kDecayCols; ++i) {
+    const int h = head(i);
+    if (row_on && h >= 0) raw[i] = dt[h];
   }
-  float suf = pre;
+  __shared__ float4 tot[kDecayCols][NH];
+  float step[kDecayCols], pre[kDecayCols], suf[kDecayCols];
+#pragma unroll
+  for (int i = 0; i < kDecayCols; ++i) {
+    const int h = head(i);
+    const bool live = row_on && h >= 0;
+    step[i] = live ? softplus(__bfloat162float(raw[i]) + (a.dt_bias ? a.dt_bias[h] : 0.f)) : 0.f;
+    pre[i] = suf[i] = live ? step[i] * (-expf(a.A_log[h]) * kLog2e) : 0.f;
+  }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float up = __shfl_up_sync(0xffffffffu, pre, o);
-    const float dn = __shfl_down_sync(0xffffffffu, suf, o);
-    if (lane >= o) pre += up;
-    if (lane < 32 - o) suf += dn;
+#pragma unroll
+    for (int i = 0; i < kDecayCols; ++i) {
+      const float up = __shfl_up_sync(0xffffffffu, pre[i], o);
+      const float dn = __shfl_down_sync(0xffffffffu, suf[i], o);
+      if (lane >= o) pre[i] += up;
+      if (lane < 32 - o) suf[i] += dn;
+    }
   }
-  suf = __shfl_down_sync(0xffffffffu, suf, 1);   // the sum over the tokens after this one
-  if (lane == 31) {
-    suf = 0.f;
-    reinterpret_cast<float*>(&tot[hs])[q] = pre;
+#pragma unroll
+  for (int i = 0; i < kDecayCols; ++i) {
+    suf[i] = __shfl_down_sync(0xffffffffu, suf[i], 1);   // the sum over the tokens after this one
+    if (lane == 31) {
+      suf[i] = 0.f;
+      reinterpret_cast<float*>(&tot[i][hs])[q] = pre[i];
+    }
   }
   __syncthreads();
-  const float4 s4 = tot[hs];
-  const float before = q == 0 ? 0.f : q == 1 ? s4.x : q == 2 ? s4.x + s4.y : s4.x + s4.y + s4.z;
-  const float after = q == 3 ? 0.f : q == 2 ? s4.w : q == 1 ? s4.z + s4.w : s4.y + s4.z + s4.w;
-  const int at = hs * 128 + t;
-  vec[VU + at] = step * tc::ex2(suf);
-  vec[VW + at] = step * tc::ex2(suf + after);
-  vec[VE + at] = tc::ex2(pre + before);
-  vec[VP + at] = pre;
-  vec[VP + 256 + at] = pre - log2_step(step);
-  if (t == 0) {
-    *reinterpret_cast<float4*>(vec + VT + hs * 4) = s4;
-    vec[VD + hs] = tc::ex2(s4.x + s4.y + s4.z + s4.w);
+#pragma unroll
+  for (int i = 0; i < kDecayCols; ++i) {
+    if (i >= ncol) break;
+    float* vec = vecs + (((long)seq * cols + col0 + i) * gridDim.y + c) * (kVec / 4);
+    const float4 s4 = tot[i][hs];
+    const float before = q == 0 ? 0.f : q == 1 ? s4.x : q == 2 ? s4.x + s4.y : s4.x + s4.y + s4.z;
+    const float after = q == 3 ? 0.f : q == 2 ? s4.w : q == 1 ? s4.z + s4.w : s4.y + s4.z + s4.w;
+    const int at = hs * 128 + t;
+    vec[VU + at] = step[i] * tc::ex2(suf[i]);
+    vec[VW + at] = step[i] * tc::ex2(suf[i] + after);
+    vec[VE + at] = tc::ex2(pre[i] + before);
+    vec[VP + at] = pre[i];
+    vec[VP + 256 + at] = pre[i] - log2_step(step[i]);
+    if (t == 0) {
+      *reinterpret_cast<float4*>(vec + VT + hs * 4) = s4;
+      vec[VD + hs] = tc::ex2(s4.x + s4.y + s4.z + s4.w);
+    }
   }
 }
 
@@ -932,7 +961,8 @@ int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
   if (!make_map(&mx, a.x, rows, (long)a.H * P, a.ldx) || !make_map(&mb, a.B, rows, (long)a.G * N, a.ldb) ||
       !make_map(&mbq, a.B, rows, (long)a.G * N, a.ldb, L / 4) || !make_map(&mc, a.C, rows, (long)a.G * N, a.ldc) || !make_map(&my, a.y, rows, (long)a.H * P, (long)a.H * P))
     return GDN_ERR_CUDA;
-  decay_kernel<NH><<<dim3((unsigned)cols, (unsigned)chunks, (unsigned)a.nseq), 128 * NH, 0, st>>>(a, vecs, next, ctas, N);
+  decay_kernel<NH><<<dim3((unsigned)((cols + kDecayCols - 1) / kDecayCols), (unsigned)chunks, (unsigned)a.nseq), 128 * NH,
+                     0, st>>>(a, vecs, next, ctas, N, cols);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (rest > 0) {
     auto first = scan_kernel<N, P, false>;
