@@ -387,6 +387,11 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         r[1] = make_int4(min(NH, hpg - pr * NH) | seg << 8, g, seq, pair);
         tc::mbar_arrive(bar(IQ + (n & 3)));
         ++n;
+        if (a.S0 && seg == 0) {                    // the item's state into L2: warpgroup 2 waits for it
+          const float* s0 = a.S0 + ((long)seq * a.H + g * hpg + pr * NH) * N * P;
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(s0), "r"(min(NH, hpg - pr * NH) * N * P * 4)
+                       : "memory");
+        }
         const float* src = k.vecs + ((long)pair * k.chunks + ch0) * (kVec / 4);
 #pragma unroll 1
         for (int c = 0; c < nc && !*abort_flag; ++c, ++cc) {
@@ -629,15 +634,11 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
     const int p = NH == 2 ? (t & 63) : t;
     const long HNP = (long)a.H * N * P;
     constexpr int kRec = N * 128 + 2;                // a segment's record
-    float S[N];                                      // row (sh, p) of S^T
-    auto publish_state = [&] {                       // the copy that the next chunk's Yi reads
-#pragma unroll
-      for (int i = 0; i < N / 8; ++i)
-        tc::st_shared_v4(sb + Lay::s + (i >> 3) * kTile + tc::sw128(t, i & 7), tc::pack_bf16(S[8 * i], S[8 * i + 1]),
-                         tc::pack_bf16(S[8 * i + 2], S[8 * i + 3]), tc::pack_bf16(S[8 * i + 4], S[8 * i + 5]),
-                         tc::pack_bf16(S[8 * i + 6], S[8 * i + 7]));
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(bar(SR));
+    uint64_t S[N / 2];                               // row (sh, p) of S^T, in pairs
+    auto packed = [&](int i) {
+      float f0, f1;
+      tc::f2_get(S[i], f0, f1);
+      return tc::pack_bf16(f0, f1);
     };
     int cc = 0;
 #pragma unroll 1
@@ -647,26 +648,27 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       const bool s_on = sh < it.heads;
       const long srow = (long)it.seq * HNP + (long)(it.h0 + sh) * N * P + p;
       float* wseg = k.ws + (long)(it.pair - k.whole) * (k.segments - 1) * kRec + t;
-      // the state before: S0, or those of the segments before, in order.  S0's loads are not waited for here: P of the
-      // item's first chunk comes before the first use of S
+      // the state before: S0, or those of the segments before, in order
       const float* from0 = it.seg == 0 ? (a.S0 ? a.S0 + srow : nullptr) : wseg;
       const int step = it.seg == 0 ? P : 128;        // distance of two state rows there
       const bool some = s_on && from0 != nullptr && (kOut || it.seg == 0);
 #pragma unroll
-      for (int i = 0; i < N; ++i) S[i] = 0.f;
+      for (int i = 0; i < N / 2; ++i) S[i] = 0;
       if (some) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) S[i] = from0[i * step];
+        for (int i = 0; i < N / 2; ++i) S[i] = tc::f2(from0[2 * i * step], from0[(2 * i + 1) * step]);
       }
       if (kOut && some && it.seg > 1) {
 #pragma unroll
-        for (int i0 = 0; i0 < N; i0 += 32) {         // 32 columns at a time: the rest of S is in registers
+        for (int i0 = 0; i0 < N / 2; i0 += 16) {     // 32 columns at a time: the rest of S is in registers
 #pragma unroll 1
           for (int s = 1; s < it.seg; ++s) {
             const float* from = wseg + (long)s * kRec;
             const float d = from[N * 128 + sh - t];
+            const uint64_t dd = tc::f2(d, d);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[i0 + i] = fmaf(d, S[i0 + i], from[(i0 + i) * 128]);
+            for (int i = 0; i < 16; ++i)
+              S[i0 + i] = tc::fma2(dd, S[i0 + i], tc::f2(from[2 * (i0 + i) * 128], from[(2 * (i0 + i) + 1) * 128]));
           }
         }
       }
@@ -675,6 +677,14 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       for (int c = 0; c < it.nc; ++c, ++cc) {
         const float* vec = vec_of(cc);
         if constexpr (kOut) {
+          // ---- the copy of S that this chunk's Yi reads, once the one before has read its own
+          if (cc > 0) wait(YI, cc - 1);
+#pragma unroll
+          for (int i = 0; i < N / 8; ++i)
+            tc::st_shared_v4(sb + Lay::s + (i >> 3) * kTile + tc::sw128(t, i & 7), packed(4 * i), packed(4 * i + 1),
+                             packed(4 * i + 2), packed(4 * i + 3));
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(bar(SR));
           // ---- P from G
           wait(GD, cc);
           tc::tc_fence_after();
@@ -741,10 +751,6 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           }
           tc::tc_fence_before();
           tc::mbar_arrive(bar(PR));
-          if (c == 0) {
-            if (cc > 0) wait(YI, cc - 1);            // Yi has read the item before's copy
-            publish_state();
-          }
         }
         // ---- S' = exp(c_L) S + U
         wait(U1, cc);
@@ -758,27 +764,31 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           tc::tmem_ld32(tlane + TU + 32 * i, U);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            tc::f2_get(tc::fma2(dd, tc::f2(S[32 * i + e], S[32 * i + e + 1]), tc::f2(U[e], U[e + 1])), S[32 * i + e],
-                       S[32 * i + e + 1]);
+          for (int e = 0; e < 16; ++e) S[16 * i + e] = tc::fma2(dd, S[16 * i + e], tc::f2(U[2 * e], U[2 * e + 1]));
         }
         tc::tc_fence_before();
         tc::mbar_arrive(bar(UR));
-        if (kOut && c + 1 < it.nc) {
-          wait(YI, cc);                              // Yi has read the copy before
-          publish_state();
-        }
       }
       // ---- the state after this item
       if (s_on) {
         if constexpr (kOut) {
           if (it.rows <= it.nc * L && a.S_T) {       // it ends its sequence
 #pragma unroll
-            for (int i = 0; i < N; ++i) a.S_T[srow + (long)i * P] = S[i];
+            for (int i = 0; i < N / 2; ++i) {
+              float f0, f1;
+              tc::f2_get(S[i], f0, f1);
+              a.S_T[srow + (long)(2 * i) * P] = f0;
+              a.S_T[srow + (long)(2 * i + 1) * P] = f1;
+            }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < N; ++i) wseg[(long)it.seg * kRec + i * 128] = S[i];
+          for (int i = 0; i < N / 2; ++i) {
+            float f0, f1;
+            tc::f2_get(S[i], f0, f1);
+            wseg[(long)it.seg * kRec + (2 * i) * 128] = f0;
+            wseg[(long)it.seg * kRec + (2 * i + 1) * 128] = f1;
+          }
           if (p == 0) wseg[(long)it.seg * kRec + N * 128 + sh - t] = seg_decay;
         }
       }
@@ -816,7 +826,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
               zr[e] = *reinterpret_cast<const uint4*>(zp + 16 * i + 8 * e);
             }
           };
-          uint4 za[2], zb[2];                        // two pieces ahead, touched by nothing before their use
+          uint4 za[2], zb[2];                        // this piece's and the next one's
           load_z(0, za);
           load_z(1, zb);
           if (gated && y_on && (c + 1) * L + t < it.rows && c + 1 < it.nc)     // the next chunk's into L2
@@ -827,7 +837,8 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           tc::tc_fence_after();
           const float e = vec_of(cc)[VE + hs * 128 + t];
           const uint64_t e2 = tc::f2(e, e);
-          auto piece = [&](int i, uint4 (&zr)[2]) {
+#pragma unroll 1
+          for (int i = 0; i < 4 && y_on; ++i) {
             float yi[16], ya[16];
             tmem_ld16(tlane + TYI + 64 * half + 16 * i, yi);
             tmem_ld16(tlane + TYA + 64 * half + 16 * i, ya);
@@ -838,7 +849,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               const uint32_t xi[4] = {xq[m].x, xq[m].y, xq[m].z, xq[m].w};
-              const uint32_t zi[4] = {zr[m].x, zr[m].y, zr[m].z, zr[m].w};
+              const uint32_t zi[4] = {za[m].x, za[m].y, za[m].z, za[m].w};
 #pragma unroll
               for (int f = 0; f < 4; ++f) {
                 const int at = 8 * m + 2 * f;
@@ -861,12 +872,9 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
               to[0] = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
               to[1] = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
             }
-            if (i < 2) load_z(i + 2, zr);
-          };
-#pragma unroll 1
-          for (int i = 0; i < 4 && y_on; i += 2) {
-            piece(i, za);
-            piece(i + 1, zb);
+            za[0] = zb[0];                           // loaded a piece ago
+            za[1] = zb[1];
+            if (i < 2) load_z(i + 2, zb);
           }
           tc::tc_fence_before();
           tc::fence_proxy_async_smem();
