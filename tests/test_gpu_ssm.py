@@ -243,6 +243,66 @@ def test_scan_packed_neighbours_stay_isolated(dtype):
     assert torch.isnan(y[100:190].float()).all() and torch.isnan(sT[1]).all()
 
 
+@pytest.mark.parametrize("P,N", [(64, 64), (128, 128)])
+def test_scan_many_short_sequences(P, N):
+    """More items than SMs: the same CTA goes from sequence to sequence, among them empty ones and longer ones."""
+    g = torch.Generator().manual_seed(71)
+    lens = torch.randint(0, 40, (330,), generator=g).tolist()
+    lens[::37] = [0] * len(lens[::37])
+    lens[5], lens[200], lens[329] = 300, 129, 256
+    H = 128 // P
+    total = sum(lens)
+    d = scan_inputs(total, len(lens), H, P, 1, N, "bf16", seed=72)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    y, sT = gdn.ssm_scan_varlen(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], cu.cuda(), max(lens), D=d["D"], z=d["z"],
+                                dt_bias=d["dt_bias"], S0=d["S0"])
+    gdn.check_error()
+    check_scan(y, sT, d, ref.spans(total, cu=cu), "bf16", True)
+    y2, s2 = gdn.ssm_scan_varlen(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], cu.cuda(), max(lens), D=d["D"], z=d["z"],
+                                 dt_bias=d["dt_bias"], S0=d["S0"])
+    assert torch.equal(y, y2) and torch.equal(sT, s2)          # whichever CTA took what
+
+
+def test_scan_whole_and_cut_pairs_together():
+    """150 pairs of (sequence, two heads): 148 run whole, two in segments."""
+    B, T, H, P, G, N = 3, 1030, 100, 64, 2, 64
+    d = scan_inputs(B * T, B, H, P, G, N, "bf16", seed=81)
+    v = {k: t.unflatten(0, (B, T)) if k in ("x", "dt", "Bm", "Cm", "z") else t for k, t in d.items()}
+    y, sT = gdn.ssm_scan(v["x"], v["dt"], v["A_log"], v["Bm"], v["Cm"], D=v["D"], z=v["z"], dt_bias=v["dt_bias"],
+                         S0=v["S0"])
+    gdn.check_error()
+    check_scan(y.flatten(0, 1), sT, d, ref.spans(B * T, B=B, T=T), "bf16", True)
+
+
+def test_scan_given_outputs_and_no_state():
+    T, H, P, G, N = 140, 2, 64, 1, 128
+    d = scan_inputs(T, 1, H, P, G, N, "bf16", seed=91)
+    one = {k: t.unsqueeze(0) if k in ("x", "dt", "Bm", "Cm", "z") else t for k, t in d.items()}
+    a = (one["x"], one["dt"], one["A_log"], one["Bm"], one["Cm"])
+    y0, s0 = gdn.ssm_scan(*a, D=d["D"], S0=d["S0"])
+    out, st = torch.empty_like(y0), torch.empty_like(s0)
+    ws = torch.empty(gdn.ssm_scan_workspace_bytes(1, T, H, G, P, N, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    y1, s1 = gdn.ssm_scan(*a, D=d["D"], S0=d["S0"], out=out, state_out=st, workspace=ws)
+    assert y1 is out and s1 is st and torch.equal(y0, y1) and torch.equal(s0, s1)
+    y2, s2 = gdn.ssm_scan(*a, D=d["D"], S0=d["S0"], want_state=False)
+    assert s2 is None and torch.equal(y0, y2)
+
+
+@pytest.mark.parametrize("P,N,dtype", [(64, 128, "bf16"), (32, 16, "f32")])
+def test_no_tokens(P, N, dtype):
+    """Without tokens the state and the history are handed on."""
+    d = scan_inputs(1, 2, 2, P, 1, N, dtype, seed=95)
+    e = {k: d[k][:0].unflatten(0, (2, 0)) for k in ("x", "dt", "Bm", "Cm")}
+    y, sT = gdn.ssm_scan(e["x"], e["dt"], d["A_log"], e["Bm"], e["Cm"], S0=d["S0"])
+    assert y.shape == (2, 0, 2, P) and torch.equal(sT, d["S0"])
+    _, s0 = gdn.ssm_scan(e["x"], e["dt"], d["A_log"], e["Bm"], e["Cm"])
+    assert (s0 == 0).all()
+    hist = torch.randn(2, 3, 8, device="cuda").to(DT[dtype])
+    out, h = gdn.ssm_conv(torch.empty(2, 0, 8, device="cuda", dtype=DT[dtype]), torch.ones(8, 4, device="cuda"),
+                          hist=hist, want_hist=True)
+    assert out.shape == (2, 0, 8) and torch.equal(h, hist)
+
+
 def test_scan_unaligned_rows_take_the_other_kernel():
     """Rows whose distance is not a multiple of 8 values (an odd number of dt columns before them)."""
     T, H, P, G, N = 140, 3, 64, 1, 64
