@@ -738,10 +738,14 @@ def _row_ld(t: Optional[torch.Tensor], lead: int, name: str) -> int:
     a contiguous tensor, or a contiguous tensor."""
     if t is None:
         return 0
-    stride = t.stride()
-    if lead == 1 and len(stride) == 2 and stride[1] == 1 and stride[0] >= t.shape[1]:
-        return stride[0]
-    shape = t.shape
+    stride, shape = t.stride(), t.shape
+    ld = stride[lead - 1]
+    if stride[-1] == 1 and (lead == 1 or stride[0] == ld * shape[1]):      # the usual layouts
+        if len(shape) == lead + 1:
+            if ld >= shape[-1]:
+                return ld
+        elif stride[-2] == shape[-1] and len(shape) == lead + 2 and ld >= shape[-1] * shape[-2]:
+            return ld
     want = 1
     for i in range(len(shape) - 1, lead - 1, -1):
         if stride[i] != want and shape[i] > 1:

@@ -85,4 +85,16 @@ __device__ __forceinline__ RowSpan row_span(const int* __restrict__ cu, int s, i
   return RowSpan{(long)a, b - a};
 }
 
+// Lets `kern` use `bytes` of dynamic shared memory; asks CUDA again only on a device, or for a size, that it has not
+// been asked for (host; one per kernel, since the kernel is the template's argument).
+template <auto kern> inline bool allow_smem(int bytes) {
+  static int allowed[64] = {};
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64 && __atomic_load_n(&allowed[dev], __ATOMIC_RELAXED) >= bytes) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64) __atomic_store_n(&allowed[dev], bytes, __ATOMIC_RELAXED);
+  return true;
+}
+
 }  // namespace gdn

@@ -57,14 +57,13 @@ void ring_add(bn::Ring& r, int i, const void* p, uint32_t bytes) {
   ++r.n;
 }
 
-template <typename Kern, typename Args>
-gdn_status launch_ring(Kern kern, const Args& a, bn::Ring ring, const Shape& s, cudaStream_t st) {
+template <auto kern, typename Args>
+gdn_status launch_ring(const Args& a, bn::Ring ring, const Shape& s, cudaStream_t st) {
   ring.stages = s.stages;
   ring.groups = s.groups;
   ring.nt = s.nt;
   const uint32_t smem = 8u * a.D + s.groups * s.stages * ring.stage_bytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return GDN_ERR_CUDA;
+  if (!allow_smem<kern>((int)smem)) return GDN_ERR_CUDA;
   kern<<<(unsigned)std::min<long>(a.rows, kSms), s.groups * s.nt, smem, st>>>(a, ring);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -84,8 +83,8 @@ gdn_status fwd(const bn::FwdArgs& a, bool vec, cudaStream_t st) {
     bn::fwd_loop_kernel<T, TH><<<(unsigned)std::min<long>(a.rows, kSms * 8), bn::kLoopThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
   }
-  if (s.k == 1) return launch_ring(bn::fwd_kernel<T, TH, 1, 768>, a, ring, s, st);
-  return launch_ring(bn::fwd_kernel<T, TH, 2, 768>, a, ring, s, st);
+  if (s.k == 1) return launch_ring<bn::fwd_kernel<T, TH, 1, 768>>(a, ring, s, st);
+  return launch_ring<bn::fwd_kernel<T, TH, 2, 768>>(a, ring, s, st);
 }
 
 template <typename T, typename TH>
@@ -109,9 +108,9 @@ gdn_status bwd(const bn::BwdArgs& a, bool vec, float* dw_post, float* dw_pre, fl
     if (cudaGetLastError() != cudaSuccess) s = GDN_ERR_CUDA;
   } else {
     parts = std::min<long>(a.rows, kSms) * sh.groups;
-    s = sh.k == 1 ? launch_ring(bn::bwd_kernel<T, TH, 1, 768>, a, ring, sh, st)
-        : sh.groups * sh.nt <= 384 ? launch_ring(bn::bwd_kernel<T, TH, 2, 384>, a, ring, sh, st)
-                                   : launch_ring(bn::bwd_kernel<T, TH, 2, 512>, a, ring, sh, st);
+    s = sh.k == 1 ? launch_ring<bn::bwd_kernel<T, TH, 1, 768>>(a, ring, sh, st)
+        : sh.groups * sh.nt <= 384 ? launch_ring<bn::bwd_kernel<T, TH, 2, 384>>(a, ring, sh, st)
+                                   : launch_ring<bn::bwd_kernel<T, TH, 2, 512>>(a, ring, sh, st);
   }
   if (s != GDN_OK) return s;
   if (!dw_post && !dw_pre && !dscale) return GDN_OK;

@@ -973,18 +973,14 @@ int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
                      0, st>>>(a, vecs, next, ctas, N, cols);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (rest > 0) {
-    auto first = scan_kernel<N, P, false>;
-    if (cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, false>::alloc) != cudaSuccess)
-      return GDN_ERR_CUDA;
+    if (!allow_smem<scan_kernel<N, P, false>>(Layout<N, false>::alloc)) return GDN_ERR_CUDA;
     k.items = (int)cut_items;
-    first<<<(unsigned)ctas.x, kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mbq, mc, my, k);
+    scan_kernel<N, P, false><<<(unsigned)ctas.x, kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mbq, mc, my, k);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   }
-  auto kern = scan_kernel<N, P, true>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, true>::alloc) != cudaSuccess)
-    return GDN_ERR_CUDA;
+  if (!allow_smem<scan_kernel<N, P, true>>(Layout<N, true>::alloc)) return GDN_ERR_CUDA;
   k.items = (int)items;
-  kern<<<(unsigned)ctas.y, kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mbq, mc, my, k);
+  scan_kernel<N, P, true><<<(unsigned)ctas.y, kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mbq, mc, my, k);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
