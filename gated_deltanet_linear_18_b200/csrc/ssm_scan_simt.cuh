@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs 
   for (int i = 0; i < NR; ++i) S[i] = a.S0 ? a.S0[sbase + (long)(ng * NR + i) * P] : 0.f;
 
   T rb[kNB], rc[kNB], rx[kNX], rt;               // the next tile, as loaded
+  T rz[kNX];                                     // this tile's gate values
   auto fetch = [&](int t0) {
     const int nt = min(kTile, sp.len - t0);
 #pragma unroll
@@ -96,6 +97,13 @@ __global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs 
       s_fade[tid] = expf(step * rate);
     }
     __syncthreads();
+    if (z) {
+#pragma unroll
+      for (int k = 0; k < kNX; ++k) {
+        const int i = tid + k * kSimtThreads, t = i / PT, p = i % PT;
+        if (t < nt) rz[k] = z[(sp.row0 + t0 + t) * a.ldz + p];
+      }
+    }
     fetch(t0 + kTile);
     auto token = [&](int t) {
       const float fade = s_fade[t], xd = sx[t][col] * s_step[t];
@@ -114,14 +122,16 @@ __global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs 
     }
     for (; t < nt; ++t) token(t);
     __syncthreads();
-    for (int i = tid; i < nt * PT; i += kSimtThreads) {
-      const int t = i / PT, p = i % PT;
-      const long r = sp.row0 + t0 + t;
-      float o = skip * sx[t][p];
 #pragma unroll
-      for (int q = 0; q < NG; ++q) o += part[t][q][p];
-      if (z) o *= silu(to_f(z[r * a.ldz + p]));
-      y[r * ((long)a.H * P) + p] = from_f<T>(o);
+    for (int k = 0; k < kNX; ++k) {
+      const int i = tid + k * kSimtThreads, t = i / PT, p = i % PT;
+      if (t < nt) {
+        float o = skip * sx[t][p];
+#pragma unroll
+        for (int q = 0; q < NG; ++q) o += part[t][q][p];
+        if (z) o *= silu(to_f(rz[k]));
+        y[(sp.row0 + t0 + t) * ((long)a.H * P) + p] = from_f<T>(o);
+      }
     }
   }
   if (a.S_T) {
