@@ -10,6 +10,11 @@ namespace ssm {
 __device__ __forceinline__ float softplus(float v) {
   return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
 }
+// -exp(A_log), finite however large A_log is (a step of 0 then still leaves the state alone)
+__device__ __forceinline__ float decay_rate(float a_log) {
+  const float e = expf(a_log);
+  return -(e > 3.402823466e38f ? 3.402823466e38f : e);
+}
 // 1 / (1 + e^-v) from the hardware's 2^x and reciprocal (each within 2^-22; below 2^-126 it is 0)
 __device__ __forceinline__ float sigmoid(float v) {
   float e, r;

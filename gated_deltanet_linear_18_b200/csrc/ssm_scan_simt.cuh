@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kSimtThreads) scan_simt_kernel(const ScanArgs 
   const T* __restrict__ Cm = static_cast<const T*>(a.C) + (long)g * N;
   const T* __restrict__ z = a.z ? static_cast<const T*>(a.z) + (long)h * P + p0 : nullptr;
   T* __restrict__ y = static_cast<T*>(a.y) + (long)h * P + p0;
-  const float rate = -expf(a.A_log[h]);
+  const float rate = decay_rate(a.A_log[h]);
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const float skip = a.D ? a.D[h] : 0.f;
 

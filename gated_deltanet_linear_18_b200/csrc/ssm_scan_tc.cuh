@@ -267,7 +267,10 @@ __global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float
     const int h = head(i);
     const bool live = row_on && h >= 0;
     step[i] = live ? softplus(__bfloat162float(raw[i]) + (a.dt_bias ? a.dt_bias[h] : 0.f)) : 0.f;
-    pre[i] = suf[i] = live ? step[i] * (-expf(a.A_log[h]) * kLog2e) : 0.f;
+    // A factor below 2^-128 is 0 wherever its exponent goes into a power; held there, it leaves the sums it is part of
+    // as accurate as their other terms are large.
+    const float v = live ? step[i] * decay_rate(a.A_log[h]) * kLog2e : 0.f;
+    pre[i] = suf[i] = v < -128.f ? -128.f : v;
   }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(DecodeShape<N, P>::NT) step_kernel(const StepA
   }
   const float step = softplus(to_f(static_cast<const T*>(a.dt)[n * a.lddt + h]) +
                               (a.dt_bias ? a.dt_bias[h] : 0.f));
-  const float fade = expf(-step * expf(a.A_log[h]));
+  const float fade = expf(step * decay_rate(a.A_log[h]));
   __syncthreads();
   float4 xd = *reinterpret_cast<const float4*>(&sx[cg * 4]);
   xd.x *= step; xd.y *= step; xd.z *= step; xd.w *= step;
