@@ -20,16 +20,17 @@ bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 struct Shape {
   int k, nt, groups, stages;
 };
-// Pieces a thread: the forward one up to 2048 columns and two above, the backward one up to 6144 (768 threads: its
-// column sums and the row are registers); as many groups as make 768 threads, fewer where a row stage for each does
-// not fit beside the vectors.  groups = 0: the width is not walked.
-int pieces(int D, bool) { return D <= 2048 ? 1 : 2; }
-int group_threads(int D, bool backward) {
-  const int k = pieces(D, backward);
+// One piece a thread up to 2048 columns, two above (8192 x 6144 bf16: the forward 100 us with two, 111 with three or
+// four; the backward 203 with two in 384 threads, 218 with one in 768).  As many groups as make 768 threads (512 where
+// the backward's two pieces need 128 registers), fewer where a row stage for each does not fit beside the vectors.
+// groups = 0: the width is not walked.
+int pieces(int D) { return D <= 2048 ? 1 : 2; }
+int group_threads(int D) {
+  const int k = pieces(D);
   return ((D / 8 + k - 1) / k + 31) / 32 * 32;
 }
 int most_groups(int D, bool backward) {
-  return std::max(1, std::min(bn::kMaxGroups, (backward && pieces(D, true) == 2 ? 512 : 768) / group_threads(D, backward)));
+  return std::max(1, std::min(bn::kMaxGroups, (backward && pieces(D) == 2 ? 512 : 768) / group_threads(D)));
 }
 Shape shape_of(int D, uint32_t row_bytes, bool backward) {
   if (D % 8 != 0 || D > 8192) return Shape{0, 0, 0, 0};
@@ -37,7 +38,7 @@ Shape shape_of(int D, uint32_t row_bytes, bool backward) {
   int groups = most_groups(D, backward);
   while (groups > 1 && room / (groups * row_bytes) < 1) --groups;
   const int stages = (int)std::min<uint32_t>(bn::kMaxStages, room / (groups * row_bytes));
-  return stages < 1 ? Shape{0, 0, 0, 0} : Shape{pieces(D, backward), group_threads(D, backward), groups, stages};
+  return stages < 1 ? Shape{0, 0, 0, 0} : Shape{pieces(D), group_threads(D), groups, stages};
 }
 // Parts of the backward's column sums that the workspace holds: the most of its two kernels, each of which
 // writes one a group or CTA.

@@ -235,6 +235,8 @@ gdn_status gdn_ssm_step(const void* u, long long ldu, const void* dt, long long 
   if (!u || !dt || !hist_in || !hist_out || hist_in == hist_out || !w || !A_log || !S || !y || ldu < C || lddt < H ||
       (z && ldz < HP))
     return GDN_ERR_INVALID_ARG;
+  // every head's CTA reads its group's rows of u and hist_in while others write
+  if (y == u || y == dt || y == z || y == hist_in || y == hist_out || y == S || hist_out == u) return GDN_ERR_INVALID_ARG;
   const void* ts[] = {u, dt, z, hist_in, hist_out, y};
   for (const void* p : ts)
     if (!aligned(p, el)) return GDN_ERR_INVALID_ARG;

@@ -646,7 +646,7 @@ GDN_API size_t gdn_ssm_scan_workspace_bytes(int nseq, int max_seqlen, int H, int
  *   u [n, H P + 2 G N]: raw rows [x | B | C]; dt [n, H]; z [n, H, P] or NULL            (dtype)
  *   hist_in, hist_out [n, 3, H P + 2 G N] (dtype): must not overlap (swap them between steps)
  *   w [H P + 2 G N, 4], bias [H P + 2 G N] or NULL, A_log, D, dt_bias as above
- *   S [n, H, N, P] float, in place; y [n, H, P] (dtype)
+ *   S [n, H, N, P] float, in place; y [n, H, P] (dtype); no output may overlap an input
  */
 GDN_API gdn_status gdn_ssm_step(const void *u, long long ldu, const void *dt, long long lddt,
                         const void *z, long long ldz, const void *hist_in, void *hist_out,

@@ -93,7 +93,8 @@ def step(L, u=FAKE, ldu=512, dt=FAKE, lddt=4, z=None, ldz=0, hin=FAKE, hout=P(0x
     (dict(n=-1), INVALID), (dict(H=3), INVALID), (dict(dtype=5), INVALID), (dict(Pd=20), UNSUPPORTED),
     (dict(u=None), INVALID), (dict(hin=None), INVALID), (dict(hout=None), INVALID), (dict(hout=FAKE), INVALID),
     (dict(w=None), INVALID), (dict(A=None), INVALID), (dict(S=None), INVALID), (dict(S=P(0x100008)), INVALID),
-    (dict(y=None), INVALID), (dict(ldu=511), INVALID), (dict(lddt=3), INVALID), (dict(z=FAKE, ldz=4), INVALID),
+    (dict(y=None), INVALID), (dict(y=FAKE), INVALID), (dict(y=P(0x200000)), INVALID),     # y over u, over a history
+    (dict(ldu=511), INVALID), (dict(lddt=3), INVALID), (dict(z=FAKE, ldz=4), INVALID),
     (dict(u=P(0x100001)), INVALID), (dict(n=0), OK),
 ])
 def test_step_validation(g, kw, expect):
