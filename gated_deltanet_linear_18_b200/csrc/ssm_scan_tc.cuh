@@ -88,17 +88,19 @@ template <int N, bool kOut> struct Layout {
   static constexpr uint32_t s = c + (kOut ? NB * kTile : 0);
   static constexpr uint32_t xw = s + (kOut ? NB * kTile : 0);       // [2 slots][3 terms][2] quarter tiles
   static constexpr uint32_t vec = xw + 2 * kSlot;
-  static constexpr uint32_t bars = vec + 3 * kVec;
+  static constexpr int kVecs = kOut ? 3 : 4;                        // chunks whose vectors are here
+  static constexpr uint32_t bars = vec + kVecs * kVec;
   static constexpr uint32_t queue = bars + 320;                     // [4] items of 32 bytes
   static constexpr uint32_t bytes = queue + 4 * 32;
   static constexpr uint32_t alloc = bytes + 1024;                   // the base is rounded up to 1024
   static_assert(alloc <= 232448, "shared memory of a CTA");
 };
 
-// Barriers.  By TMA: XF (two x tiles), BF (B's four quarters; without outputs two buffers), CF, VR (three vector
-// slots).  By warp 0: IQ (four items).  By MMA commits: UQ (the two X' slots read), U1 (U complete), BE (the same parts of
+// Barriers.  By TMA: XF (two x tiles), BF (B's four quarters; without outputs two buffers), CF, VR (three or four
+// vector slots).  By warp 0: IQ (four items).  By MMA commits: UQ (the two X' slots read), U1 (U complete), BE (the same parts of
 // B read by U), BX (two: U complete and so x's tile read for X'), GD (G), YI, YA.  By the threads of the warpgroups: XT
-// (two X' slots staged), PR (P), UR (U is in registers), SR (the state operand), YR (two: y in its tile, Yi and Ya read).
+// (two X' slots staged), PR (P), UR (U is in registers; without outputs two, by
+// place), SR (the state operand), YR (two: y in its tile, Yi and Ya read).
 // A wait names a phase by its parity alone, so each one below stands where the phase after the awaited
 // one cannot have completed: what completes that needs something this waiter has yet to do.  For the same
 // reason YR and BX are kept by tile, only warp 3 waits for XT and only warpgroup 1 for VR; G, U and Y being complete
@@ -111,8 +113,8 @@ __device__ __forceinline__ float log2_step(float v) {
 }
 
 enum Bar {
-  XF = 0, BF = 2, CF = BF + 4, UQ, U1 = UQ + 2, BE, BX = BE + 4, GD = BX + 2, YI, YA, VR, IQ = VR + 3, DRAIN = IQ + 4,
-  XT, PR = XT + 2, UR, SR, YR, kBars = YR + 2
+  XF = 0, BF = 2, CF = BF + 4, UQ, U1 = UQ + 2, BE, BX = BE + 4, GD = BX + 2, YI, YA, VR, IQ = VR + 4, DRAIN = IQ + 4,
+  XT, PR = XT + 2, UR, SR = UR + 2, YR, kBars = YR + 2
 };
 
 // Bounded wait in few instructions (there are many of them, and the roles' code has to stay in the instruction
@@ -320,7 +322,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   constexpr int NH = 128 / P;                 // heads of this CTA
   constexpr int NB = N / 64;
   constexpr uint32_t TG = 0, TYI = 128, TYA = 256, TU = kOut ? 384 : 0;
-  constexpr uint32_t kTmem = kOut ? 512 : 128;
+  constexpr uint32_t kTmem = kOut ? 512 : 256;   // (without outputs U has two places)
   const ScanArgs& a = k.a;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -346,7 +348,8 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   const int wg = warp >> 2, q = warp & 3;                 // warpgroup; lane quadrant
   const int t = tid & 127;                                // a token's (or hp's) row
   const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
-  auto vec_of = [&](int cc) { return reinterpret_cast<float*>(smem + Lay::vec + (cc % 3) * kVec); };
+  constexpr int kV = Lay::kVecs;
+  auto vec_of = [&](int cc) { return reinterpret_cast<float*>(smem + Lay::vec + (cc % kV) * kVec); };
   // The n-th item of this CTA, for every role but warp 0, which writes it.  Four slots: warp 0 writes item n + 4 when
   // the last chunk of item n + 3 is being loaded, and so after every role has done with chunks three before that.
   struct Item {
@@ -398,11 +401,11 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         const float* src = k.vecs + ((long)pair * k.chunks + ch0) * (kVec / 4);
 #pragma unroll 1
         for (int c = 0; c < nc && !*abort_flag; ++c, ++cc) {
-          // the vectors' slot held chunk cc - 3's, which every role is through with: this thread has seen (with outputs) Yi
-          // of cc - 2, issued after y of cc - 3, or U of cc - 3 or later, issued after the state of the chunk before it
+          // the vectors' slot held chunk cc - kV's, which every role is through with: this thread has seen (with outputs)
+          // Yi of cc - 2, issued after y of cc - 3, or U of cc - 2, issued after the state of cc - 4
           if (!kOut && cc >= 2) wait(BE + (cc & 1), (cc >> 1) - 1);
-          tc::mbar_arrive_expect_tx(bar(VR + cc % 3), kVec);
-          tc::bulk_load(sb + Lay::vec + (cc % 3) * kVec, src + (long)c * (kVec / 4), kVec, bar(VR + cc % 3));
+          tc::mbar_arrive_expect_tx(bar(VR + cc % kV), kVec);
+          tc::bulk_load(sb + Lay::vec + (cc % kV) * kVec, src + (long)c * (kVec / 4), kVec, bar(VR + cc % kV));
           const int row = row0 + c * L;
           if constexpr (kOut) {
             // There is room for one B tile: a quarter of the next one takes its place as soon as U and G have read that
@@ -433,7 +436,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
         } else {
           for (int i = max(0, cc - 2); i < cc; ++i) bounded_wait(bar(BF + (i & 1)), (i >> 1) & 1, &never);
         }
-        for (int i = max(0, cc - 3); i < cc; ++i) bounded_wait(bar(VR + i % 3), (i / 3) & 1, &never);
+        for (int i = max(0, cc - kV); i < cc; ++i) bounded_wait(bar(VR + i % kV), (i / kV) & 1, &never);
       }
     } else if (warp == 2 && lane == 0) {
       // --------------------------------- x and y -----------------------------------------------
@@ -497,7 +500,9 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           const int bbuf = kOut ? 0 : cc & 1;
           const uint64_t dbt = tc::desc_adv(db0, bbuf * NB * kTile);
           if (!kOut) wait(BF + bbuf, cc >> 1);
-          if (cc > 0) wait(UR, cc - 1);
+          if (kOut && cc > 0) wait(UR, cc - 1);
+          if (!kOut && cc > 1) wait(UR + bbuf, (cc >> 1) - 1);
+          const uint32_t tu = tmem + TU + bbuf * 128;
           // a quarter of the chunk's tokens: 2 steps of 16 for each of the three terms
 #pragma unroll 1
           for (int qd = 0; qd < 4; ++qd) {
@@ -507,12 +512,12 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
             const uint64_t dw = tc::desc_adv(dxw, (qd & 1) * kSlot), dq = tc::desc_adv(dbt, qd * (kTile / 4));
 #pragma unroll
             for (int i = 0; i < 6; ++i)
-              mma_ss(tmem + TU, tc::desc_adv(dw, (i >> 1) * (kTile / 2) + (i & 1) * 2048), tc::desc_adv(dq, (i & 1) * 2048),
+              mma_ss(tu, tc::desc_adv(dw, (i >> 1) * (kTile / 2) + (i & 1) * 2048), tc::desc_adv(dq, (i & 1) * 2048),
                      ID_U, qd + i > 0, leader);
             commit(bar(UQ + (qd & 1)), leader);
             if (kOut) commit(bar(BE + qd), leader);
           }
-          commit(bar(U1), leader);
+          if (kOut) commit(bar(U1), leader);
           commit(bar(BX + (cc & 1)), leader);
           if (!kOut) commit(bar(BE + bbuf), leader);
         }
@@ -585,7 +590,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
 #pragma unroll 1
       for (int c = 0; c < it.nc; ++c, ++cc) {
         const int valid = min(L, it.rows - c * L);
-        wait(VR + cc % 3, cc / 3);
+        wait(VR + cc % kV, cc / kV);
         wait(XF + (cc & 1), cc >> 1);
         if (kOut && valid < L) {   // rows behind the sequence reach no product: another sequence's, maybe NaN
           // (G may be reading B meanwhile: it yields columns s >= valid, which no row t < valid keeps)
@@ -756,21 +761,23 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           tc::mbar_arrive(bar(PR));
         }
         // ---- S' = exp(c_L) S + U
-        wait(U1, cc);
+        if (kOut) wait(U1, cc);
+        else wait(BX + (cc & 1), cc >> 1);           // (U runs up to two chunks ahead: kept by place)
         tc::tc_fence_after();
+        const uint32_t tu = tlane + TU + (kOut ? 0 : (cc & 1) * 128);
         const float d = vec[VD + sh];
         seg_decay *= d;
         const uint64_t dd = tc::f2(d, d);
 #pragma unroll
         for (int i = 0; i < N / 32; ++i) {
           float U[32];
-          tc::tmem_ld32(tlane + TU + 32 * i, U);
+          tc::tmem_ld32(tu + 32 * i, U);
           tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) S[16 * i + e] = tc::fma2(dd, S[16 * i + e], tc::f2(U[2 * e], U[2 * e + 1]));
         }
         tc::tc_fence_before();
-        tc::mbar_arrive(bar(UR));
+        tc::mbar_arrive(bar(UR + (kOut ? 0 : cc & 1)));
       }
       // ---- the state after this item
       if (s_on) {
