@@ -220,6 +220,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// The launches of a call overlap: each one lets the next be placed as soon as its own CTAs all run, and the next sets
+// its barriers and TMEM up before it waits for the launch before to have completed (which has waited likewise).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The decay vectors of every chunk: grid (blocks of kDecayCols columns, chunks, sequences), 128 threads for each of a
 // column's heads, a token a thread and a block of 32 tokens a warp.  The columns of a block share the sectors of a
 // token's dt row, all loaded before the first is used.  It also sets the item counters of the launches that follow, and
@@ -232,6 +237,7 @@ __global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float
   const int c = blockIdx.y, seq = blockIdx.z;
   const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
   const int hs = threadIdx.x >> 7, t = threadIdx.x & 127, q = t >> 5, lane = t & 31;
+  launch_dependents();
   if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x == 0) {
     next[0] = first.x;
     next[1] = first.y;
@@ -344,6 +350,8 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  dependency_wait();         // what the launch before wrote is read from here on
+  if (!kOut) launch_dependents();
   auto wait = [&](int b, int phase) { bounded_wait(bar(b), (uint32_t)phase & 1u, abort_flag); };
   const int wg = warp >> 2, q = warp & 3;                 // warpgroup; lane quadrant
   const int t = tid & 127;                                // a token's (or hp's) row
@@ -960,6 +968,24 @@ inline Space space(int nseq, int max_len, int H, int G, int P, int N) {
   return Space{256 + states, 256 + states + pairs * chunks * kVec};
 }
 
+// A launch that may be placed before the one before it in its stream has completed.
+template <auto kern, typename... A>
+bool launch_after(int ctas, int smem, cudaStream_t st, const A&... args) {
+  if (!allow_smem<kern>(smem)) return false;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)ctas);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, kern, args...);
+  return cudaGetLastError() == cudaSuccess;
+}
+
 template <int N, int P>
 int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
   constexpr int NH = 128 / P;
@@ -983,15 +1009,13 @@ int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
                      0, st>>>(a, vecs, next, ctas, N, cols);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (rest > 0) {
-    if (!allow_smem<scan_kernel<N, P, false>>(Layout<N, false>::alloc)) return GDN_ERR_CUDA;
     k.items = (int)cut_items;
-    scan_kernel<N, P, false><<<(unsigned)ctas.x, kThreads, Layout<N, false>::alloc, st>>>(mx, mb, mbq, mc, my, k);
-    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    if (!launch_after<scan_kernel<N, P, false>>(ctas.x, Layout<N, false>::alloc, st, mx, mb, mbq, mc, my, k))
+      return GDN_ERR_CUDA;
   }
-  if (!allow_smem<scan_kernel<N, P, true>>(Layout<N, true>::alloc)) return GDN_ERR_CUDA;
   k.items = (int)items;
-  scan_kernel<N, P, true><<<(unsigned)ctas.y, kThreads, Layout<N, true>::alloc, st>>>(mx, mb, mbq, mc, my, k);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return launch_after<scan_kernel<N, P, true>>(ctas.y, Layout<N, true>::alloc, st, mx, mb, mbq, mc, my, k) ? GDN_OK
+                                                                                                          : GDN_ERR_CUDA;
 }
 
 }  // namespace tcs
