@@ -85,15 +85,15 @@ __device__ __forceinline__ RowSpan row_span(const int* __restrict__ cu, int s, i
   return RowSpan{(long)a, b - a};
 }
 
-// Lets `kern` use `bytes` of dynamic shared memory; asks CUDA again only on a device, or for a size, that it has not
-// been asked for (host; one per kernel, since the kernel is the template's argument).
-template <auto kern> inline bool allow_smem(int bytes) {
+// Lets `kern` use up to `bytes` of dynamic shared memory, always the same number for a kernel (calls of several threads
+// may come here at once); asks CUDA once per device (host; one per kernel, since the kernel is the template's argument).
+template <auto kern, int bytes> inline bool allow_smem() {
   static int allowed[64] = {};
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  if (dev >= 0 && dev < 64 && __atomic_load_n(&allowed[dev], __ATOMIC_RELAXED) >= bytes) return true;
+  if (dev >= 0 && dev < 64 && __atomic_load_n(&allowed[dev], __ATOMIC_RELAXED)) return true;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-  if (dev >= 0 && dev < 64) __atomic_store_n(&allowed[dev], bytes, __ATOMIC_RELAXED);
+  if (dev >= 0 && dev < 64) __atomic_store_n(&allowed[dev], 1, __ATOMIC_RELAXED);
   return true;
 }
 

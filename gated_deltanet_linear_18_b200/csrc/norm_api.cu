@@ -64,7 +64,7 @@ gdn_status launch_ring(const Args& a, bn::Ring ring, const Shape& s, cudaStream_
   ring.groups = s.groups;
   ring.nt = s.nt;
   const uint32_t smem = 8u * a.D + s.groups * s.stages * ring.stage_bytes;
-  if (!allow_smem<kern>((int)smem)) return GDN_ERR_CUDA;
+  if (!allow_smem<kern, (int)kSmem>()) return GDN_ERR_CUDA;
   kern<<<(unsigned)std::min<long>(a.rows, kSms), s.groups * s.nt, smem, st>>>(a, ring);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -969,9 +969,9 @@ inline Space space(int nseq, int max_len, int H, int G, int P, int N) {
 }
 
 // A launch that may be placed before the one before it in its stream has completed.
-template <auto kern, typename... A>
-bool launch_after(int ctas, int smem, cudaStream_t st, const A&... args) {
-  if (!allow_smem<kern>(smem)) return false;
+template <auto kern, int smem, typename... A>
+bool launch_after(int ctas, cudaStream_t st, const A&... args) {
+  if (!allow_smem<kern, smem>()) return false;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
@@ -1010,12 +1010,12 @@ int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (rest > 0) {
     k.items = (int)cut_items;
-    if (!launch_after<scan_kernel<N, P, false>>(ctas.x, Layout<N, false>::alloc, st, mx, mb, mbq, mc, my, k))
+    if (!launch_after<scan_kernel<N, P, false>, (int)Layout<N, false>::alloc>(ctas.x, st, mx, mb, mbq, mc, my, k))
       return GDN_ERR_CUDA;
   }
   k.items = (int)items;
-  return launch_after<scan_kernel<N, P, true>>(ctas.y, Layout<N, true>::alloc, st, mx, mb, mbq, mc, my, k) ? GDN_OK
-                                                                                                          : GDN_ERR_CUDA;
+  return launch_after<scan_kernel<N, P, true>, (int)Layout<N, true>::alloc>(ctas.y, st, mx, mb, mbq, mc, my, k)
+             ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace tcs

@@ -235,3 +235,32 @@ def test_zero_rows():
     assert ho.shape == x.shape == (0, 64)
     g = gdn.block_norm_bwd(e, e, e, e, w_post=w, w_pre=w)
     assert (g["dw_post"] == 0).all() and (g["dw_pre"] == 0).all()
+
+
+def test_threads_with_widths_of_their_own():
+    """Calls of several threads at once, each on its own stream, whose kernels need different amounts of shared
+    memory: what each gets alone."""
+    import threading
+    widths = [2056, 4096, 6144, 8192]
+    ds = [inputs(3, D, "bf16", "bf16", True, True, True, True, seed=D) for D in widths]
+    got, errors = [None] * len(ds), []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got[i] = gdn.block_norm(ds[i]["y"], ds[i]["h"], eps=EPS, **opts(ds[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:                               # noqa: BLE001 (told to the test's own thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(ds))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for d, (ho, x) in zip(ds, got):
+        h1, x1 = gdn.block_norm(d["y"], d["h"], eps=EPS, **opts(d))
+        assert torch.equal(ho, h1) and torch.equal(x, x1)
