@@ -19,6 +19,10 @@
 // groups are added by a second kernel in a fixed order: reproducible bit for bit.  Rows whose width
 // is not a multiple of 8 values, or whose tensors are not 16-byte aligned, take the loop kernels at
 // the end.
+// Measured, 8192 x 6144 bf16, gate and both vectors: forward 100 us = 5.0 TB/s (a copy: 6.45), backward 203 us = 4.0
+// TB/s.  The backward is short of warps: its 158 registers a thread (40 of raw values, 32 of column sums, 16 of
+// sigmoids) leave 12 an SM, which issue in 43 % of the cycles and wait for the row's sums in between.  With
+// two syncs a row it took 214 us, with a row a CTA, read again in each pass, 240 (the forward so: 181).
 #pragma once
 
 #include "common.cuh"

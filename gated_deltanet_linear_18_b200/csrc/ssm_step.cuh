@@ -9,7 +9,8 @@
 // four columns (one float4) of the rows rg, rg + RG, ..., all of whose loads are issued before the
 // convolution is computed, so that the row's work hides under them.  The heads of a group each
 // recompute its B and C (8 N values against 8 N P bytes of state); the group's first head moves
-// their history on.
+// their history on.  Measured, bf16: 256 sequences of 48 heads of 128 x 128 in 262 us = 6.3 TB/s, the rate
+// of a copy; one of 64 heads of 128 x 64 in 3.9 us, the latency of its loads and sums.
 #pragma once
 
 #include "decode.cuh"
