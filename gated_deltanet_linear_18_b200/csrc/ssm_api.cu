@@ -14,6 +14,8 @@ namespace {
 
 using bf = __nv_bfloat16;
 
+constexpr int kMostPacked = 1 << 30;   // rows of a packed call: a row and a length add up in 32 bits
+
 bool valid_dtype(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
 bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 size_t elem(gdn_dtype t) { return t == GDN_F32 ? 4 : 2; }
@@ -46,6 +48,8 @@ gdn_status conv_call(const void* x, long long ldx, const float* w, const float* 
                      gdn_stream_t stream) {
   if (nseq < 0 || T < 0 || max_len < 0 || C <= 0 || !valid_dtype(dtype)) return GDN_ERR_INVALID_ARG;
   const long rows = cu ? (long)T : (long)nseq * T;
+  if (cu && T > kMostPacked) return GDN_ERR_UNSUPPORTED;
+  if (cu) max_len = std::min(max_len, T);
   if (nseq == 0 || (rows == 0 && !hist_out)) return GDN_OK;
   const size_t el = elem(dtype);
   if (rows > 0 && (!x || !out || !w || ldx < C)) return GDN_ERR_INVALID_ARG;
@@ -109,6 +113,7 @@ gdn_status scan_call(ssm::ScanArgs a, int P, int N, void* workspace, size_t work
   if (a.nseq == 0) return GDN_OK;
   if (a.nseq > 65535) return GDN_ERR_UNSUPPORTED;
   const long rows = a.cu ? (long)a.T : (long)a.nseq * a.T;
+  if (a.cu && a.T > kMostPacked) return GDN_ERR_UNSUPPORTED;
   const size_t el = elem(dtype);
   if (!a.A_log || !aligned(a.A_log, 4) || !aligned(a.D, 4) || !aligned(a.dt_bias, 4) || !aligned(a.S0, 16) ||
       !aligned(a.S_T, 16) || (a.S_T && a.S_T == a.S0))
@@ -125,6 +130,7 @@ gdn_status scan_call(ssm::ScanArgs a, int P, int N, void* workspace, size_t work
   const size_t need = scan_workspace(a.nseq, a.max_len, a.H, a.G, P, N, dtype);
   if (need && rows > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return GDN_ERR_INVALID_ARG;
+  if (a.cu) a.max_len = std::min(a.max_len, a.T);      // (needs no more scratch than what was asked for)
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const void* tiles[] = {a.x, a.B, a.C, a.z};
   bool tc = dtype == GDN_BF16 && ssm::tcs::supported(P, N) && rows > 0 && rows <= 0x7fffffffL - 2 * ssm::tcs::L &&

@@ -136,11 +136,13 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a) {
   }
 
   const long rows = a.cu ? (long)a.T : (long)a.nseq * a.T;
-  const long first = (long)blockIdx.x * a.tile;
+  long first = (long)blockIdx.x * a.tile;
   const long last = min(first + a.tile, rows);
   int s = seq_of_row(a.cu, a.nseq, a.T, first);
   long r0, r1;
   seq_rows(a.cu, s, a.T, a.max_len, r0, r1);
+  first = max(first, r0);              // rows before the first sequence are in none
+  if (first >= last) return;
 
   f2_t w[4][NP], b[NP];
   {

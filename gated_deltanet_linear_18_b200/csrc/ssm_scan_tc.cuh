@@ -957,7 +957,7 @@ struct Cut {
 };
 inline Cut cut(int nseq, int max_len, int H, int G, int P) {
   const long n = (long)nseq * columns(H, G, P), rest = n % 148;
-  const int chunks = (max_len + L - 1) / L;
+  const int chunks = max_len / L + (max_len % L != 0);
   if (rest == 0 || n > 148 * 5) return Cut{(int)n, 1};
   const long s = 148 / rest < chunks / 4 ? 148 / rest : chunks / 4;
   return s < 2 ? Cut{(int)n, 1} : Cut{(int)(n - rest), (int)s};

@@ -599,7 +599,7 @@ GDN_API gdn_status gdn_ssm_conv(const void *x, long long ldx, const float *w, co
 
 /* gdn_ssm_conv over packed sequences: x, out [total_T, C]; cu_seqlens, max_seqlen as
  * gdn_chunk_fwd_varlen; hist_in, hist_out [nseq, 3, C].  No sequence reads a neighbour's rows; rows
- * in no sequence keep their out. */
+ * in no sequence keep their out.  Packed calls of this block take 2^30 rows at most. */
 GDN_API gdn_status gdn_ssm_conv_varlen(const void *x, long long ldx, const float *w,
                         const float *bias, const int *cu_seqlens, int nseq, int max_seqlen,
                         const void *hist_in, void *out, void *hist_out, int total_T, int C,

@@ -84,6 +84,68 @@ def test_conv_packed_rows_behind_and_empty(dtype, lens):
     assert (out[total - behind:] == 7.0).all()
 
 
+@pytest.mark.parametrize("lead", [1, 2, 5, 70])
+def test_packed_sequences_that_start_behind_the_first_row(lead):
+    """Rows before the first sequence belong to none: they reach no window and keep their outputs."""
+    lens, C = [9, 0, 70, 3], 40
+    total = lead + sum(lens)
+    d = conv_inputs(total, C, len(lens), "bf16", seed=lead)
+    cu = torch.tensor([lead] + lens).cumsum(0).to(torch.int32)
+    for hist in (d["hist"], None):
+        out = torch.full((total, C), 7.0, dtype=torch.bfloat16, device="cuda")
+        _, hout = gdn.ssm_conv_varlen(d["x"], d["w"], d["bias"], cu.cuda(), 70, hist=hist, want_hist=True, out=out)
+        want, hwant, mag = ref.conv(d["x"], d["w"], d["bias"], hist, ref.spans(total, cu=cu))
+        check_conv(out, want, mag, "bf16")
+        assert torch.equal(hout.cpu().double(), hwant) and (out[:lead] == 7.0).all()
+    for P, N, dtype in ((64, 64, "bf16"), (16, 16, "f32")):
+        d = scan_inputs(total, len(lens), 2, P, 1, N, dtype, seed=lead)
+        out = torch.full((total, 2, P), 7.0, device="cuda", dtype=DT[dtype])
+        y, sT = gdn.ssm_scan_varlen(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], cu.cuda(), 70, D=d["D"], z=d["z"],
+                                    dt_bias=d["dt_bias"], S0=d["S0"], out=out)
+        check_scan(y, sT, d, ref.spans(total, cu=cu), dtype, uses_tensor_cores(P, N, dtype))
+        assert (out[:lead] == 7.0).all()
+
+
+def test_packed_calls_with_the_largest_max_seqlen():
+    """A max_seqlen that no sequence comes near, up to 2^31 - 1: what the longest one's length gives."""
+    lens = [5, 40, 3]
+    total, most = sum(lens), 2 ** 31 - 1
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    d = conv_inputs(total, 24, 3, "bf16", seed=61)
+    call = lambda m: gdn.ssm_conv_varlen(d["x"], d["w"], d["bias"], cu, m, hist=d["hist"], want_hist=True)
+    for a, b in zip(call(40), call(most)):
+        assert torch.equal(a, b)
+    for dtype, m in (("f32", most), ("bf16", 5000)):
+        s = scan_inputs(total, 3, 2, 64, 1, 64, dtype, seed=62)
+        scan = lambda m: gdn.ssm_scan_varlen(s["x"], s["dt"], s["A_log"], s["Bm"], s["Cm"], cu, m, D=s["D"], S0=s["S0"])
+        for a, b in zip(scan(40), scan(m)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_packed_sequences_longer_than_told(dtype):
+    """A sequence takes max_seqlen rows at most; the rows behind them belong to none."""
+    lens, most, H, P, G, N = [90, 40, 200], 64, 2, 64, 1, 64
+    total = sum(lens)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    sp = ref.spans(total, cu=cu, max_len=most)
+    inside = torch.zeros(total, dtype=torch.bool)
+    for a, b in sp:
+        inside[a:b] = True
+    d = conv_inputs(total, 24, 3, dtype, seed=6)
+    out = torch.full((total, 24), 7.0, dtype=DT[dtype], device="cuda")
+    _, hout = gdn.ssm_conv_varlen(d["x"], d["w"], d["bias"], cu.cuda(), most, hist=d["hist"], want_hist=True, out=out)
+    want, hwant, mag = ref.conv(d["x"], d["w"], d["bias"], d["hist"], sp)
+    check_conv(out, want, mag, dtype)
+    assert torch.equal(hout.cpu().double(), hwant) and (out.cpu()[~inside] == 7.0).all()
+    d = scan_inputs(total, 3, H, P, G, N, dtype, seed=7)
+    out = torch.full((total, H, P), 7.0, device="cuda", dtype=DT[dtype])
+    y, sT = gdn.ssm_scan_varlen(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], cu.cuda(), most, D=d["D"], z=d["z"],
+                                dt_bias=d["dt_bias"], S0=d["S0"], out=out)
+    check_scan(y, sT, d, sp, dtype, uses_tensor_cores(P, N, dtype))
+    assert (out.cpu()[~inside] == 7.0).all()
+
+
 def test_conv_large_takes_long_tiles_and_equals_short_ones():
     """A call whose tiles are long gives what its pieces (tiles of a few rows) give, bit for bit, with the
     history handed on."""

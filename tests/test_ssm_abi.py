@@ -43,6 +43,11 @@ def test_varlen_calls_need_offsets(g):
     ptr = [FAKE, 128, FAKE, 2, FAKE, 64, FAKE, 64, None, 0, FAKE, None, None]
     assert L.gdn_ssm_scan_varlen(*ptr, None, 1, 4, None, P(0x200000), None, FAKE, 1 << 40, 4, 2, 1, 64, 64, 1,
                                  None) == INVALID
+    many = (1 << 30) + 1                                         # a row and a length have to add up in 32 bits
+    assert L.gdn_ssm_conv_varlen(FAKE, 64, FAKE, None, FAKE, 1, 4, None, P(0x200000), None, many, 64, 1,
+                                 None) == UNSUPPORTED
+    assert L.gdn_ssm_scan_varlen(*ptr, FAKE, 1, 4, None, P(0x200000), None, FAKE, 1 << 40, many, 2, 1, 64, 64, 1,
+                                 None) == UNSUPPORTED
 
 
 def scan(L, x=FAKE, ldx=256, dt=FAKE, lddt=4, Bm=FAKE, ldb=128, Cm=FAKE, ldc=128, z=None, ldz=0, A=FAKE, D=None,
