@@ -565,3 +565,35 @@ def test_step_in_a_graph_with_swapped_histories():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[2]) and torch.equal(got[1], want[3]) and torch.equal(Sg, Se)
+
+
+def test_scans_of_two_threads_at_once():
+    """Scans that fill the GPU each, on streams and workspaces of their own: what each gets alone."""
+    import threading
+    cases = []
+    for i, (P, N, T, H) in enumerate([(64, 128, 1500, 6), (128, 64, 700, 5), (64, 64, 2100, 40)]):
+        d = scan_inputs(T, 1, H, P, 1, N, "bf16", seed=110 + i)
+        one = {k: t.unsqueeze(0) if k in ("x", "dt", "Bm", "Cm", "z") else t for k, t in d.items()}
+        cases.append((one["x"], one["dt"], one["A_log"], one["Bm"], one["Cm"], dict(D=d["D"], z=one["z"], S0=d["S0"])))
+    alone = [gdn.ssm_scan(*c[:5], **c[5]) for c in cases]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(cases), []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i] = gdn.ssm_scan(*cases[i][:5], **cases[i][5])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:                               # noqa: BLE001 (told to the test's own thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    gdn.check_error()
+    assert not errors, errors
+    for (y, s), (y0, s0) in zip(got, alone):
+        assert torch.equal(y, y0) and torch.equal(s, s0)
