@@ -9,9 +9,10 @@
 // and the three-row window stay in registers, and the next kConvBatch rows are loaded while the present
 // ones are computed.  A tile is as long as one wave of CTAs allows, since a thread's 5 VEC taps and biases
 // are as many bytes as ten rows of bf16.  Only the window's three rows are read twice.
-// Measured, 16384 x 6144 bf16: 90 us = 4.5 TB/s (a copy: 6.45); 161 us with tiles of 32 rows.  Rows ahead
-// and CTAs an SM: 2 and 4 95 us, 2 and 5 104, 4 and 5 125, 8 and 3 92; a branch for four rows of one
-// sequence, without the question of each row's sequence, 107 (it spills).
+// Measured, 16384 x 6144 bf16: 88-90 us = 4.5 TB/s (a copy: 6.45), issuing in 61 % of the cycles; 161 us with
+// tiles of 32 rows.  Rows ahead and CTAs an SM: 2 and 4 95 us, 2 and 5 104, 4 and 5 125, 8 and 3 92; 8-byte
+// pieces with twice the warps 104; a branch for four rows of one sequence, without the question of each
+// row's sequence, 107 (it spills).
 #pragma once
 
 #include "ssm_common.cuh"
