@@ -42,8 +42,8 @@
 // states before it, combined in order (the result does not depend on timing).  That is done for the (sequence,
 // column) pairs that do not fill a wave of the SMs: 192 of them run as 148 whole ones and 44 in three segments.
 //
-// Measured (bf16): 8192 tokens of 64 heads of 128 x 64, gated, 142 us (decays 9, first launch 37, second 97); 4 x 2048
-// tokens of 48 heads of 128 x 128, 114 us; a ragged batch of 32 prompts of 64 heads, gated, 161 us.  A chunk takes
+// Measured (bf16): 8192 tokens of 64 heads of 128 x 64, gated, 139 us (decays 8, first launch 37, second 97); 4 x 2048
+// tokens of 48 heads of 128 x 128, 112-117 us; a ragged batch of 32 prompts of 64 heads, gated, 160 us.  A chunk takes
 // about 5 us.  352 KB of MMA operands and about as much of tiles pass through shared memory in it (2.9 us at 128 bytes a
 // cycle); the rest is what the roles wait for one another and for instructions.
 #pragma once
@@ -234,7 +234,8 @@ __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol
 // column's heads, a token a thread and a block of 32 tokens a warp.  The columns of a block share the sectors of a
 // token's dt row, all loaded before the first is used.  It also sets the item counters of the launches that follow, and
 // hands the state of a sequence without tokens on.
-constexpr int kDecayCols = 8;
+// (8192 x 64 heads: 139 us with two or four columns, 141 with eight; ragged batch 162, 160 and 161.)
+constexpr int kDecayCols = 4;
 template <int NH>
 __global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float* __restrict__ vecs, int* next, int2 first, int N,
                                                          int cols) {
