@@ -108,8 +108,9 @@ template <int N, bool kOut> struct Layout {
 // place), SR (the state operand), YR (two: y in its tile, Yi and Ya read).
 // A wait names a phase by its parity alone, so each one below stands where the phase after the awaited
 // one cannot have completed: what completes that needs something this waiter has yet to do.  For the same
-// reason YR and BX are kept by tile, only warp 3 waits for XT and only warpgroup 1 for VR; G, U and Y being complete
-// implies the vectors for the others.
+// reason YR and BX are kept by tile and only warp 3 waits for XT.  Copies complete in any order (B and C of a chunk from
+// L2 may be there before its vectors), so every role that reads the vectors waits for VR itself, in vectors(); a slot's
+// next copy is issued only after all of them have read this one.
 // log2 of a time step (0 gives -infinity: that token's weight is 0)
 __device__ __forceinline__ float log2_step(float v) {
   float r;
@@ -363,7 +364,11 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
   const int t = tid & 127;                                // a token's (or hp's) row
   const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
   constexpr int kV = Lay::kVecs;
-  auto vec_of = [&](int cc) { return reinterpret_cast<float*>(smem + Lay::vec + (cc % kV) * kVec); };
+  // The decay vectors of chunk cc, once their copy has landed.
+  auto vectors = [&](int cc) {
+    wait(VR + cc % kV, cc / kV);
+    return reinterpret_cast<const float*>(smem + Lay::vec + (cc % kV) * kVec);
+  };
   // The n-th item of this CTA, for every role but warp 0, which writes it.  Four slots: warp 0 writes item n + 4 when
   // the last chunk of item n + 3 is being loaded, and so after every role has done with chunks three before that.
   struct Item {
@@ -416,7 +421,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
 #pragma unroll 1
         for (int c = 0; c < nc && !*abort_flag; ++c, ++cc) {
           // the vectors' slot held chunk cc - kV's, which every role is through with: this thread has seen (with outputs)
-          // Yi of cc - 2, issued after y of cc - 3, or U of cc - 2, issued after the state of cc - 4
+          // Yi of cc - 2, issued after y and the state of cc - 3, or U of cc - 2, issued after the state of cc - 4
           if (!kOut && cc >= 2) wait(BE + (cc & 1), (cc >> 1) - 1);
           tc::mbar_arrive_expect_tx(bar(VR + cc % kV), kVec);
           tc::bulk_load(sb + Lay::vec + (cc % kV) * kVec, src + (long)c * (kVec / 4), kVec, bar(VR + cc % kV));
@@ -604,7 +609,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
 #pragma unroll 1
       for (int c = 0; c < it.nc; ++c, ++cc) {
         const int valid = min(L, it.rows - c * L);
-        wait(VR + cc % kV, cc / kV);
+        const float* vec = vectors(cc);
         wait(XF + (cc & 1), cc >> 1);
         if (kOut && valid < L) {   // rows behind the sequence reach no product: another sequence's, maybe NaN
           // (G may be reading B meanwhile: it yields columns s >= valid, which no row t < valid keeps)
@@ -618,7 +623,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           // three bf16 terms that add up to the fp32 product
           const uint32_t from = sb + Lay::x + ((cc & 1) * 2 + tile) * kTile + qd * (kTile / 4);
           const uint32_t dst = sb + Lay::xw + slot * kSlot + tile * (kTile / 4);
-          const float* w_ = vec_of(cc) + VW + (NH == 2 ? tile : 0) * 128 + qd * 32;
+          const float* w_ = vec + VW + (NH == 2 ? tile : 0) * 128 + qd * 32;
 #pragma unroll 2
           for (int r = r0; r < 32; r += 8) {
             uint4 xv = tc::ld_shared_v4(from + tc::sw128(r, j));
@@ -697,7 +702,6 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
       float seg_decay = 1.f;
 #pragma unroll 1
       for (int c = 0; c < it.nc; ++c, ++cc) {
-        const float* vec = vec_of(cc);
         if constexpr (kOut) {
           // ---- the copy of S that this chunk's Yi reads, once the one before has read its own
           if (cc > 0) wait(YI, cc - 1);
@@ -707,6 +711,9 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
                              packed(4 * i + 2), packed(4 * i + 3));
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(bar(SR));
+        }
+        const float* vec = vectors(cc);
+        if constexpr (kOut) {
           // ---- P from G
           wait(GD, cc);
           tc::tc_fence_after();
@@ -859,7 +866,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           wait(BX + (cc & 1), cc >> 1);              // warpgroup 1 has read x's tile: y may take its place
           wait(YA, cc);
           tc::tc_fence_after();
-          const float e = vec_of(cc)[VE + hs * 128 + t];
+          const float e = vectors(cc)[VE + hs * 128 + t];
           const uint64_t e2 = tc::f2(e, e);
 #pragma unroll 1
           for (int i = 0; i < 4 && y_on; ++i) {

@@ -1,0 +1,36 @@
+"""The state space block's calls at the edges of their ranges: decay vectors beyond the L2 cache, bounds on the
+sequences' lengths that no sequence comes near, the most rows of a packed call, and what the token step keeps in fp32."""
+import pytest
+import torch
+
+import gated_deltanet_linear_18_b200 as gdn
+
+pytestmark = pytest.mark.gpu
+
+
+def test_scan_results_do_not_depend_on_the_order_of_the_sequences():
+    """24 sequences of 64 heads, none cut: chunks' vectors, B, C and x come from HBM or L2 as it happens, on whichever
+    SM takes them.  The sequences in another order give every one the same bits."""
+    H, P, G, N = 64, 64, 1, 128
+    g = torch.Generator().manual_seed(131)
+    lens = torch.randint(900, 2049, (24,), generator=g)
+    total, most = int(lens.sum()), int(lens.max())
+    cg = torch.Generator(device="cuda").manual_seed(132)
+    rows = torch.randn(total, H * P + 2 * G * N + H, generator=cg, device="cuda").to(torch.bfloat16)
+    A_log = torch.log(torch.rand(H, generator=g) * 15 + 1).cuda()
+    order = torch.randperm(24, generator=g)
+
+    def run(rows, lens):
+        cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)]).to(torch.int32).cuda()
+        x, Bm, Cm, dt = rows.split([H * P, G * N, G * N, H], -1)
+        y, sT = gdn.ssm_scan_varlen(x.unflatten(1, (H, P)), dt, A_log, Bm.unflatten(1, (G, N)), Cm.unflatten(1, (G, N)),
+                                    cu, most)
+        return y, sT
+
+    y0, s0 = run(rows, lens)
+    at = [int(v) for v in lens.cumsum(0) - lens]
+    index = torch.cat([torch.arange(at[s], at[s] + int(lens[s])) for s in order]).cuda()
+    for _ in range(3):
+        y1, s1 = run(rows[index], lens[order])
+        assert torch.equal(y1, y0[index]) and torch.equal(s1, s0[order.cuda()])
+    gdn.check_error()
