@@ -77,12 +77,12 @@ struct RowSpan {
   long row0;
   int len;
 };
-__device__ __forceinline__ RowSpan row_span(const int* __restrict__ cu, int s, int T,
-                                            int max_len) {
+__host__ __device__ __forceinline__ RowSpan row_span(const int* __restrict__ cu, int s, int T,
+                                                     int max_len) {
   if (!cu) return RowSpan{(long)s * T, T};
   const int a = min(max(cu[s], 0), T);
-  const int b = min(max(cu[s + 1], a), min(T, a + max_len));
-  return RowSpan{(long)a, b - a};
+  const int room = min(T - a, max_len);            // (a + max_len may be beyond 2^31 - 1)
+  return RowSpan{(long)a, min(max(cu[s + 1], a) - a, room)};
 }
 
 // Lets `kern` use up to `bytes` of dynamic shared memory, always the same number for a kernel (calls of several threads

@@ -14,7 +14,7 @@ namespace {
 
 using bf = __nv_bfloat16;
 
-constexpr int kMostPacked = 1 << 30;   // rows of a packed call: a row and a length add up in 32 bits
+constexpr int kMostPacked = 1 << 30;   // rows of a packed call: a row and the tile or chunk behind it fit in 32 bits
 
 bool valid_dtype(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
 bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }

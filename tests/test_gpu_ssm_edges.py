@@ -34,3 +34,21 @@ def test_scan_results_do_not_depend_on_the_order_of_the_sequences():
         y1, s1 = run(rows[index], lens[order])
         assert torch.equal(y1, y0[index]) and torch.equal(s1, s0[order.cuda()])
     gdn.check_error()
+
+
+def test_conv_over_the_most_packed_rows():
+    """2^30 rows of one channel, the sequence behind them empty: it hands its history on, and the last rows are those
+    of a short call."""
+    T = 2 ** 30
+    g = torch.Generator(device="cuda").manual_seed(141)
+    x = torch.randn(T, 1, generator=g, device="cuda", dtype=torch.bfloat16)
+    w, bias = torch.randn(1, 4, generator=g, device="cuda"), torch.randn(1, generator=g, device="cuda")
+    hist = torch.randn(2, 3, 1, generator=g, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, T, T], dtype=torch.int32, device="cuda")
+    tail = gdn.ssm_conv(x[None, -5000:], w, bias)[0, 3:]
+    out = torch.empty_like(x)
+    for most in (T, 2 ** 31 - 1):
+        out.zero_()
+        _, h = gdn.ssm_conv_varlen(x, w, bias, cu, most, hist=hist, want_hist=True, out=out)
+        assert torch.equal(h[0], x[-3:]) and torch.equal(h[1], hist[1])
+        assert torch.equal(out[-4997:], tail)
