@@ -101,7 +101,7 @@ gdn_status check_heads(int H, int G, int P, int N) {
 }
 
 size_t scan_workspace(int nseq, int max_len, int H, int G, int P, int N, gdn_dtype dtype) {
-  if (dtype != GDN_BF16 || !ssm::tcs::supported(P, N)) return 0;
+  if (nseq <= 0 || max_len <= 0 || dtype != GDN_BF16 || !ssm::tcs::supported(P, N)) return 0;
   return ssm::tcs::space(nseq, max_len, H, G, P, N).bytes;
 }
 
@@ -200,7 +200,7 @@ gdn_status gdn_ssm_conv_varlen(const void* x, long long ldx, const float* w, con
 }
 
 size_t gdn_ssm_scan_workspace_bytes(int nseq, int max_seqlen, int H, int G, int P, int N, gdn_dtype dtype) {
-  if (nseq <= 0 || max_seqlen <= 0 || !valid_dtype(dtype) || check_heads(H, G, P, N) != GDN_OK) return 0;
+  if (!valid_dtype(dtype) || check_heads(H, G, P, N) != GDN_OK) return 0;
   return scan_workspace(nseq, max_seqlen, H, G, P, N, dtype);
 }
 

@@ -52,3 +52,20 @@ def test_conv_over_the_most_packed_rows():
         _, h = gdn.ssm_conv_varlen(x, w, bias, cu, most, hist=hist, want_hist=True, out=out)
         assert torch.equal(h[0], x[-3:]) and torch.equal(h[1], hist[1])
         assert torch.equal(out[-4997:], tail)
+
+
+@pytest.mark.parametrize("P,N,dtype", [(64, 128, torch.bfloat16), (128, 64, torch.bfloat16), (32, 16, torch.float32)])
+def test_packed_calls_with_a_bound_of_zero_over_rows_in_no_sequence(P, N, dtype):
+    """Empty sequences only, in a padded batch: states and histories are handed on, the rows keep their outputs."""
+    n, rows, H = 3, 5, 2
+    g = torch.Generator(device="cuda").manual_seed(151)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    cu = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    t = lambda *s: r(*s).to(dtype)
+    S0, y = r(n, H, N, P), torch.full((rows, H, P), 7.0, dtype=dtype, device="cuda")
+    assert gdn.ssm_scan_workspace_bytes(n, 0, H, 1, P, N, dtype) == 0
+    _, sT = gdn.ssm_scan_varlen(t(rows, H, P), t(rows, H), r(H), t(rows, 1, N), t(rows, 1, N), cu, 0, S0=S0, out=y)
+    assert torch.equal(sT, S0) and (y == 7.0).all()
+    hist, out = t(n, 3, 24), torch.full((rows, 24), 7.0, dtype=dtype, device="cuda")
+    _, h = gdn.ssm_conv_varlen(t(rows, 24), r(24, 4), None, cu, 0, hist=hist, want_hist=True, out=out)
+    assert torch.equal(h, hist) and (out == 7.0).all()
