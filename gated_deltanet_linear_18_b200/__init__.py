@@ -138,6 +138,8 @@ def lib() -> ctypes.CDLL:
             fn.restype = I
         L.gdn_ssm_scan_workspace_bytes.argtypes = [I] * 7
         L.gdn_ssm_scan_workspace_bytes.restype = SZ
+        L.gdn_ssm_scan_varlen_workspace_bytes.argtypes = [I] * 8
+        L.gdn_ssm_scan_varlen_workspace_bytes.restype = SZ
         L.gdn_block_norm_bwd_workspace_bytes.argtypes = [LL, I]
         L.gdn_block_norm_bwd_workspace_bytes.restype = SZ
         _lib = L
@@ -834,8 +836,11 @@ def ssm_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, *, hist=None, want_
     return (out, hist_out) if want_hist else out
 
 
-def ssm_scan_workspace_bytes(nseq, max_seqlen, H, G, P, N, dtype) -> int:
-    """Device scratch bytes ``ssm_scan`` / ``ssm_scan_varlen`` need (0: none)."""
+def ssm_scan_workspace_bytes(nseq, max_seqlen, H, G, P, N, dtype, total: Optional[int] = None) -> int:
+    """Device scratch bytes ``ssm_scan`` / ``ssm_scan_varlen`` need (0: none); with ``total``, the rows of
+    a packed call, no more than its rows make necessary."""
+    if total is not None:
+        return int(lib().gdn_ssm_scan_varlen_workspace_bytes(nseq, max_seqlen, total, H, G, P, N, _DTYPES[dtype]))
     return int(lib().gdn_ssm_scan_workspace_bytes(nseq, max_seqlen, H, G, P, N, _DTYPES[dtype]))
 
 
@@ -870,7 +875,10 @@ def _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, lead, nseq, max_len, want_sta
     sT = state_out
     if sT is None and want_state:
         sT = A_log.new_empty((nseq, H, N, P))
-    need = (_lib or lib()).gdn_ssm_scan_workspace_bytes(nseq, max_len, H, G, P, N, io)
+    if cu is None:
+        need = (_lib or lib()).gdn_ssm_scan_workspace_bytes(nseq, max_len, H, G, P, N, io)
+    else:
+        need = (_lib or lib()).gdn_ssm_scan_varlen_workspace_bytes(nseq, max_len, shape[0], H, G, P, N, io)
     ws, wbytes = _workspace(need, x.device, workspace)
     head = (x.data_ptr(), lds[0], dt.data_ptr(), lds[1], Bm.data_ptr(), lds[2], Cm.data_ptr(), lds[3], _ptr(z),
             lds[4], A_log.data_ptr(), _ptr(D), _ptr(dt_bias))

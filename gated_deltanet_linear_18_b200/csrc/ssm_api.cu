@@ -100,9 +100,10 @@ gdn_status check_heads(int H, int G, int P, int N) {
   return GDN_OK;
 }
 
-size_t scan_workspace(int nseq, int max_len, int H, int G, int P, int N, gdn_dtype dtype) {
+// total: rows of a packed call; -1: not known, or not packed
+size_t scan_workspace(int nseq, int max_len, long total, int H, int G, int P, int N, gdn_dtype dtype) {
   if (nseq <= 0 || max_len <= 0 || dtype != GDN_BF16 || !ssm::tcs::supported(P, N)) return 0;
-  return ssm::tcs::space(nseq, max_len, H, G, P, N).bytes;
+  return ssm::tcs::space(nseq, max_len, total, H, G, P, N).bytes;
 }
 
 gdn_status scan_call(ssm::ScanArgs a, int P, int N, void* workspace, size_t workspace_bytes, gdn_dtype dtype,
@@ -127,10 +128,10 @@ gdn_status scan_call(ssm::ScanArgs a, int P, int N, void* workspace, size_t work
       if (!aligned(p, el) || p == a.y) return GDN_ERR_INVALID_ARG;
     if (!aligned(a.y, 16)) return GDN_ERR_INVALID_ARG;
   }
-  const size_t need = scan_workspace(a.nseq, a.max_len, a.H, a.G, P, N, dtype);
+  if (a.cu) a.max_len = std::min(a.max_len, a.T);
+  const size_t need = scan_workspace(a.nseq, a.max_len, a.cu ? rows : -1L, a.H, a.G, P, N, dtype);
   if (need && rows > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return GDN_ERR_INVALID_ARG;
-  if (a.cu) a.max_len = std::min(a.max_len, a.T);      // (needs no more scratch than what was asked for)
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const void* tiles[] = {a.x, a.B, a.C, a.z};
   bool tc = dtype == GDN_BF16 && ssm::tcs::supported(P, N) && rows > 0 && rows <= 0x7fffffffL - 2 * ssm::tcs::L &&
@@ -201,7 +202,13 @@ gdn_status gdn_ssm_conv_varlen(const void* x, long long ldx, const float* w, con
 
 size_t gdn_ssm_scan_workspace_bytes(int nseq, int max_seqlen, int H, int G, int P, int N, gdn_dtype dtype) {
   if (!valid_dtype(dtype) || check_heads(H, G, P, N) != GDN_OK) return 0;
-  return scan_workspace(nseq, max_seqlen, H, G, P, N, dtype);
+  return scan_workspace(nseq, max_seqlen, -1L, H, G, P, N, dtype);
+}
+
+size_t gdn_ssm_scan_varlen_workspace_bytes(int nseq, int max_seqlen, int total_T, int H, int G, int P, int N,
+                                           gdn_dtype dtype) {
+  if (total_T < 0 || !valid_dtype(dtype) || check_heads(H, G, P, N) != GDN_OK) return 0;
+  return scan_workspace(nseq, std::min(max_seqlen, total_T), total_T, H, G, P, N, dtype);
 }
 
 gdn_status gdn_ssm_scan(const void* x, long long ldx, const void* dt, long long lddt, const void* Bm, long long ldb,

@@ -65,12 +65,26 @@ constexpr uint32_t kTile = L * 128;           // bytes of a [128 rows, 64 bf16] 
 using bf16_t = __nv_bfloat16;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Where the chunks of a sequence have their records, `n` in all for a column.  Each sequence has room for the longest
+// one's `chunks`; or, where a packed call's rows make that fewer, sequence s starts at record (its first row) / L + s:
+// behind the last one of every sequence before it, since floor(len / L) + 1 >= ceil(len / L), and below total / L + nseq.
+struct Records {
+  long n;
+  int chunks, by_rows;
+  __host__ __device__ long first(int seq, long row0) const { return by_rows ? row0 / L + seq : (long)seq * chunks; }
+};
+inline Records records_of(int nseq, int max_len, long total) {     // total < 0: not known, or not packed
+  const int chunks = max_len / L + (max_len % L != 0);
+  const long each = (long)nseq * chunks, by_rows = total / L + nseq;
+  return total >= 0 && by_rows < each ? Records{by_rows, chunks, 1} : Records{each, chunks, 0};
+}
+
 struct Args {
   ScanArgs a;
   int* next;                    // the next item of each launch (set by the decay kernel)
   float* ws;                    // [pairs cut][segments - 1] of a state [N][128] and two decays
-  const float* vecs;            // decay vectors: [pairs][chunks] records of kVec bytes
-  int chunks;                   // chunks of the longest sequence
+  const float* vecs;            // decay vectors: [columns][records.n] records of kVec bytes
+  Records records;
   int columns, whole;           // pair = sequence * columns + column; the first `whole` pairs are not cut
   int seg_chunks, segments;     // the others: chunks of a segment, segments of the longest sequence
   int items;                    // of this launch
@@ -231,20 +245,29 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The decay vectors of every chunk: grid (blocks of kDecayCols columns, chunks, sequences), 128 threads for each of a
-// column's heads, a token a thread and a block of 32 tokens a warp.  The columns of a block share the sectors of a
-// token's dt row, all loaded before the first is used.  It also sets the item counters of the launches that follow, and
-// hands the state of a sequence without tokens on.
+// The decay vectors of every chunk: grid (blocks of kDecayCols columns, records as y + z gridDim.y: the chunks of sequence z
+// where records are not by rows), 128 threads for each of a column's heads, a token a thread and a block of 32 tokens a
+// warp.  The columns of a block share the sectors of a token's dt row, all loaded before the first is used.  It also sets
+// the item counters of the launches that follow, and hands the state of a sequence without tokens on.
 // (8192 x 64 heads: 139 us with two or four columns, 141 with eight; ragged batch 162, 160 and 161.)
 constexpr int kDecayCols = 4;
 template <int NH>
-__global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float* __restrict__ vecs, int* next, int2 first, int N,
-                                                         int cols) {
-  const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH;
-  const int c = blockIdx.y, seq = blockIdx.z;
-  const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
-  const int hs = threadIdx.x >> 7, t = threadIdx.x & 127, q = t >> 5, lane = t & 31;
+__global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, const Records rec, float* __restrict__ vecs, int* next,
+                                                         int2 first, int N, int cols) {
   launch_dependents();
+  const int hpg = a.H / a.G, pairs = (hpg + NH - 1) / NH;
+  const long record = (long)blockIdx.z * gridDim.y + blockIdx.y;
+  int seq = blockIdx.z;
+  if (rec.by_rows) {                       // the last sequence that starts at this record or before
+    seq = 0;
+    for (int hi = a.nseq - 1; seq < hi;) {
+      const int mid = (seq + hi + 1) >> 1;
+      if (rec.first(mid, row_span(a.cu, mid, a.T, a.max_len).row0) <= record) seq = mid; else hi = mid - 1;
+    }
+  }
+  const RowSpan sp = row_span(a.cu, seq, a.T, a.max_len);
+  const int c = rec.by_rows ? (int)(record - rec.first(seq, sp.row0)) : (int)blockIdx.y;
+  const int hs = threadIdx.x >> 7, t = threadIdx.x & 127, q = t >> 5, lane = t & 31;
   if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x == 0) {
     next[0] = first.x;
     next[1] = first.y;
@@ -255,7 +278,7 @@ __global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float
     const int g = (col0 + i) / pairs, in = ((col0 + i) % pairs) * NH + hs;
     return i < ncol && in < hpg ? g * hpg + in : -1;
   };
-  if (c * L >= sp.len) {
+  if (record >= rec.n || c < 0 || (long)c * L >= sp.len) {       // (c < 0: offsets that decrease)
     if (sp.len == 0 && c == 0 && a.S_T) {
       for (int i = 0; i < ncol; ++i) {
         const int h = head(i);
@@ -309,7 +332,7 @@ __global__ void __launch_bounds__(128 * NH) decay_kernel(const ScanArgs a, float
 #pragma unroll
   for (int i = 0; i < kDecayCols; ++i) {
     if (i >= ncol) break;
-    float* vec = vecs + (((long)seq * cols + col0 + i) * gridDim.y + c) * (kVec / 4);
+    float* vec = vecs + ((col0 + i) * rec.n + record) * (kVec / 4);
     const float4 s4 = tot[i][hs];
     const float before = q == 0 ? 0.f : q == 1 ? s4.x : q == 2 ? s4.x + s4.y : s4.x + s4.y + s4.z;
     const float after = q == 3 ? 0.f : q == 2 ? s4.w : q == 1 ? s4.z + s4.w : s4.y + s4.z + s4.w;
@@ -417,7 +440,7 @@ scan_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUte
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(s0), "r"(min(NH, hpg - pr * NH) * N * P * 4)
                        : "memory");
         }
-        const float* src = k.vecs + ((long)pair * k.chunks + ch0) * (kVec / 4);
+        const float* src = k.vecs + (col * k.records.n + k.records.first(seq, sp.row0) + ch0) * (kVec / 4);
 #pragma unroll 1
         for (int c = 0; c < nc && !*abort_flag; ++c, ++cc) {
           // the vectors' slot held chunk cc - kV's, which every role is through with: this thread has seen (with outputs)
@@ -970,15 +993,16 @@ inline Cut cut(int nseq, int max_len, int H, int G, int P) {
   const long s = 148 / rest < chunks / 4 ? 148 / rest : chunks / 4;
   return s < 2 ? Cut{(int)n, 1} : Cut{(int)(n - rest), (int)s};
 }
-// The workspace: the item counters (256 bytes), segment states and decays, the decay vectors.
+// The workspace: the item counters (256 bytes), segment states and decays, the decay vectors (total: rows of a packed
+// call, -1 where that is not known).
 struct Space {
   size_t vecs, bytes;
 };
-inline Space space(int nseq, int max_len, int H, int G, int P, int N) {
+inline Space space(int nseq, int max_len, long total, int H, int G, int P, int N) {
   const Cut c = cut(nseq, max_len, H, G, P);
-  const size_t pairs = (size_t)nseq * columns(H, G, P), chunks = ((size_t)max_len + L - 1) / L;
+  const size_t cols = (size_t)columns(H, G, P), pairs = nseq * cols;
   const size_t states = ((pairs - c.whole) * (c.segments - 1) * (N * 128 + 2) * sizeof(float) + 255) / 256 * 256;
-  return Space{256 + states, 256 + states + pairs * chunks * kVec};
+  return Space{256 + states, 256 + states + cols * records_of(nseq, max_len, total).n * kVec};
 }
 
 // A launch that may be placed before the one before it in its stream has completed.
@@ -1003,23 +1027,26 @@ template <int N, int P>
 int launch_np(const ScanArgs& a, void* ws, cudaStream_t st) {
   constexpr int NH = 128 / P;
   const long rows = a.cu ? (long)a.T : (long)a.nseq * a.T;
-  const int chunks = (a.max_len + L - 1) / L;
+  const long total = a.cu ? (long)a.T : -1L;
+  const Records rec = records_of(a.nseq, a.max_len, total);
   const Cut ct = cut(a.nseq, a.max_len, a.H, a.G, P);
   const int cols = columns(a.H, a.G, P);
   const long pairs = (long)a.nseq * cols, rest = pairs - ct.whole;
-  float* vecs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + space(a.nseq, a.max_len, a.H, a.G, P, N).vecs);
+  float* vecs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + space(a.nseq, a.max_len, total, a.H, a.G, P, N).vecs);
   int* next = static_cast<int*>(ws);
-  Args k{a, next, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256), vecs, chunks, cols, ct.whole,
-         (chunks + ct.segments - 1) / ct.segments, ct.segments, 0};
+  Args k{a, next, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256), vecs, rec, cols, ct.whole,
+         (rec.chunks + ct.segments - 1) / ct.segments, ct.segments, 0};
   const long cut_items = rest * (ct.segments - 1), items = ct.whole + rest * ct.segments;
   if (items > 0x3fffffffL) return GDN_ERR_UNSUPPORTED;
+  // records over y and z (by rows there are 2^23 + nseq at most, otherwise nseq of at most 65535 chunks each)
+  const long gy = rec.by_rows ? (rec.n < 65535 ? rec.n : 65535) : rec.chunks, gz = (rec.n + gy - 1) / gy;
   const int2 ctas = make_int2((int)(cut_items < 148 ? cut_items : 148), (int)(items < 148 ? items : 148));
   CUtensorMap mx, mb, mbq, mc, my;
   if (!make_map(&mx, a.x, rows, (long)a.H * P, a.ldx) || !make_map(&mb, a.B, rows, (long)a.G * N, a.ldb) ||
       !make_map(&mbq, a.B, rows, (long)a.G * N, a.ldb, L / 4) || !make_map(&mc, a.C, rows, (long)a.G * N, a.ldc) || !make_map(&my, a.y, rows, (long)a.H * P, (long)a.H * P))
     return GDN_ERR_CUDA;
-  decay_kernel<NH><<<dim3((unsigned)((cols + kDecayCols - 1) / kDecayCols), (unsigned)chunks, (unsigned)a.nseq), 128 * NH,
-                     0, st>>>(a, vecs, next, ctas, N, cols);
+  decay_kernel<NH><<<dim3((unsigned)((cols + kDecayCols - 1) / kDecayCols), (unsigned)gy, (unsigned)gz), 128 * NH, 0, st>>>(
+      a, rec, vecs, next, ctas, N, cols);
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (rest > 0) {
     k.items = (int)cut_items;

@@ -625,7 +625,7 @@ GDN_API gdn_status gdn_ssm_scan(const void *x, long long ldx, const void *dt, lo
 
 /* gdn_ssm_scan over packed sequences: [total_T, ...] token tensors, S0, S_T [nseq, H, N, P];
  * cu_seqlens, max_seqlen as gdn_chunk_fwd_varlen.  Rows in no sequence keep their y; an empty
- * sequence hands its S0 on. */
+ * sequence hands its S0 on.  workspace: gdn_ssm_scan_varlen_workspace_bytes(...) bytes. */
 GDN_API gdn_status gdn_ssm_scan_varlen(const void *x, long long ldx, const void *dt,
                         long long lddt, const void *Bm, long long ldb, const void *Cm, long long ldc,
                         const void *z, long long ldz, const float *A_log, const float *D,
@@ -635,9 +635,13 @@ GDN_API gdn_status gdn_ssm_scan_varlen(const void *x, long long ldx, const void 
                         gdn_dtype dtype, gdn_stream_t stream);
 
 /* Device scratch bytes of both scans for nseq sequences of at most max_seqlen tokens (host only,
- * no CUDA call; 0 for sizes that the calls reject). */
+ * no CUDA call; 0 for sizes that the calls reject).  gdn_ssm_scan_varlen_workspace_bytes: what a packed
+ * call over total_T rows needs, never more; it grows with the rows and not with nseq x max_seqlen, so that
+ * a max_seqlen far above every length costs no memory. */
 GDN_API size_t gdn_ssm_scan_workspace_bytes(int nseq, int max_seqlen, int H, int G, int P, int N,
                         gdn_dtype dtype);
+GDN_API size_t gdn_ssm_scan_varlen_workspace_bytes(int nseq, int max_seqlen, int total_T, int H, int G,
+                        int P, int N, gdn_dtype dtype);
 
 /*
  * One token of the block for n sequences in one kernel: the convolution over the carried history,

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import gated_deltanet_linear_18_b200 as gdn
+import ssm_ref as ref
+import test_gpu_ssm as base
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +71,46 @@ def test_packed_calls_with_a_bound_of_zero_over_rows_in_no_sequence(P, N, dtype)
     hist, out = t(n, 3, 24), torch.full((rows, 24), 7.0, dtype=dtype, device="cuda")
     _, h = gdn.ssm_conv_varlen(t(rows, 24), r(24, 4), None, cu, 0, hist=hist, want_hist=True, out=out)
     assert torch.equal(h, hist) and (out == 7.0).all()
+
+
+RAGGED = {"ragged": [0, 1, 127, 128, 129, 0, 300, 2, 0], "short": [1] * 40 + [0, 3], "one of many": [0] * 60 + [200] + [0] * 9}
+
+
+@pytest.mark.parametrize("lead,behind", [(0, 0), (3, 200)])
+@pytest.mark.parametrize("P,N", [(64, 128), (128, 64)])
+@pytest.mark.parametrize("lens", RAGGED.values(), ids=RAGGED)
+def test_packed_scan_under_a_bound_far_above_every_length(lens, P, N, lead, behind):
+    """Bounds up to 2^31 - 1: scratch as the rows make necessary, and no byte of it beyond what the query says is
+    written; results as the fp64 form's."""
+    H, G, n = 4, 2, len(lens)
+    total = lead + sum(lens) + behind
+    d = base.scan_inputs(total, n, H, P, G, N, "bf16", seed=160 + P)
+    d["z"] = d["z"].contiguous()                                    # (16-byte rows: the tensor cores' kernel)
+    cu = torch.tensor([lead] + lens).cumsum(0).to(torch.int32)
+    for most in (max(lens), total + 1000, 2 ** 31 - 1):
+        need = gdn.ssm_scan_workspace_bytes(n, most, H, G, P, N, torch.bfloat16, total=total)
+        ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")         # (NaN where not written)
+        out = torch.full((total, H, P), 7.0, device="cuda", dtype=torch.bfloat16)
+        args = (d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], cu.cuda(), most)
+        opt = dict(D=d["D"], z=d["z"], dt_bias=d["dt_bias"], S0=d["S0"])
+        y, sT = gdn.ssm_scan_varlen(*args, **opt, out=out, workspace=ws[:need])
+        gdn.check_error()
+        assert (ws[need:] == 0xFF).all() and (out[:lead] == 7.0).all() and (out[total - behind:] == 7.0).all()
+        base.check_scan(y, sT, d, ref.spans(total, cu=cu), "bf16", True)
+        y2, s2 = gdn.ssm_scan_varlen(*args, **opt, out=torch.full_like(out, 7.0))       # scratch from the allocator
+        assert torch.equal(y2, y) and torch.equal(s2, sT)
+
+
+def test_scratch_of_many_short_requests_under_one_long_bound():
+    """512 requests of a few tokens and one of 3000 under a bound of 16384: room as for the rows, and the call runs."""
+    lens = [5 + i % 13 for i in range(512)]
+    lens[300] = 3000
+    H, P, G, N, total = 8, 64, 1, 64, sum(lens)
+    d = base.scan_inputs(total, 512, H, P, G, N, "bf16", seed=171)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    y, sT = gdn.ssm_scan_varlen(d["x"], d["dt"], d["A_log"], d["Bm"], d["Cm"], cu, 16384, D=d["D"], S0=d["S0"])
+    records = H // 2 * (total // 128 + 512) * (2 * 128 * 5 + 16) * 4
+    assert torch.cuda.max_memory_allocated() - before < records + y.nbytes + sT.nbytes + (8 << 20)
+    base.check_scan(y, sT, d, ref.spans(total, cu=cu), "bf16", True, z=False, bias=False)
