@@ -5,7 +5,9 @@ import torch
 
 import gated_deltanet_linear_18_b200 as gdn
 import ssm_ref as ref
+import ssm_step_ref as step_ref
 import test_gpu_ssm as base
+import test_ssm_step_bounds as step_bounds
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +116,19 @@ def test_scratch_of_many_short_requests_under_one_long_bound():
     records = H // 2 * (total // 128 + 512) * (2 * 128 * 5 + 16) * 4
     assert torch.cuda.max_memory_allocated() - before < records + y.nbytes + sT.nbytes + (8 << 20)
     base.check_scan(y, sT, d, ref.spans(total, cu=cu), "bf16", True, z=False, bias=False)
+
+
+@pytest.mark.parametrize("full", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n,H,P,G,N", step_bounds.SHAPES, ids=str)
+def test_step_keeps_the_convolution_in_fp32(n, H, P, G, N, dtype, full):
+    """One token, each value held to a bound of its own, which bf16 between convolution and state update would break."""
+    b = step_ref.inputs(n, H, P, G, N, dtype, seed=n + H)
+    y, S, ty, tS, hist = step_ref.step(b, G, dtype, full)
+    d = {k: v.cuda() for k, v in b.items()}
+    opt = dict(D=d["D"], z=d["z"], dt_bias=d["dt_bias"]) if full else {}
+    got, nxt = gdn.ssm_step(d["u"], d["dt"], d["hist"], d["w"], d["bias"] if full else None, d["A_log"], d["S"], groups=G,
+                            **opt)
+    base.within(d["S"], S, tS, "S")
+    base.within(got, y, ty, "y")
+    assert torch.equal(nxt.cpu().double(), hist)
