@@ -730,6 +730,12 @@ def _fp32(*ts: Optional[torch.Tensor]):
             raise ValueError("gates, states and weights must be float32")
 
 
+def _fit(*sizes: int):
+    """Sizes that the C ABI takes as ints (ctypes would cut them to 32 bits without a word)."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError("sizes must be below 2^31")
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -785,6 +791,7 @@ def _call(name: str, dev: int, *args):
 
 def _conv(x, lead, w, bias, hist, nseq, want_hist, out, cu=None):
     C = x.shape[-1]
+    _fit(*x.shape)
     if w.shape != (C, 4) or (bias is not None and bias.shape != (C,)):
         raise ValueError("w must be [C, 4] and bias [C]")
     if hist is not None and (hist.shape != (nseq, 3, C) or hist.dtype != x.dtype):
@@ -829,10 +836,11 @@ def ssm_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, *, hist=None, want_
     [nseq,3,C].  Rows in no sequence keep their ``out``."""
     if x.dim() != 2:
         raise ValueError("x must be [total, C]")
-    nseq = _offsets(cu_seqlens)
+    nseq, max_seqlen = _offsets(cu_seqlens), int(max_seqlen)
+    _fit(max_seqlen)
     out, hist_out, ld, io, dev = _conv(x, 1, w, bias, hist, nseq, want_hist, out, cu_seqlens)
     _call("gdn_ssm_conv_varlen", dev, x.data_ptr(), ld, w.data_ptr(), _ptr(bias), cu_seqlens.data_ptr(), nseq,
-          int(max_seqlen), _ptr(hist), out.data_ptr(), _ptr(hist_out), x.shape[0], x.shape[1], io)
+          max_seqlen, _ptr(hist), out.data_ptr(), _ptr(hist_out), x.shape[0], x.shape[1], io)
     return (out, hist_out) if want_hist else out
 
 
@@ -854,6 +862,7 @@ def _scan(x, dt, A_log, Bm, Cm, D, z, dt_bias, S0, lead, nseq, max_len, want_sta
             or (z is not None and z.shape != shape):
         raise ValueError("x, dt, Bm, Cm, z shapes disagree")
     G, N = bs[lead:]
+    _fit(max_len, G, N, *shape)
     ty = x.dtype
     if dt.dtype != ty or Bm.dtype != ty or Cm.dtype != ty or (z is not None and z.dtype != ty):
         raise ValueError("x, dt, Bm, Cm, z must have one dtype")
@@ -963,6 +972,7 @@ def ssm_step(u, dt, hist, w, bias, A_log, S, *, groups: int, D=None, z=None, dt_
 def _norm_args(y, h, z, w_post, w_pre, res_scale):
     shape = y.shape
     D = shape[-1]
+    _fit(D)
     if h.shape != shape or (z is not None and z.shape != shape):
         raise ValueError("y, h and z must have one shape")
     if z is not None and z.dtype != y.dtype:
