@@ -17,12 +17,16 @@
 // vectors (w_post s, w_pre) sit in shared memory, read from HBM once per CTA; a thread owns the same
 // 8 K columns in every row, so the backward's two column sums stay in registers.  The sums of the
 // groups are added by a second kernel in a fixed order: reproducible bit for bit.  Rows whose width
-// is not a multiple of 8 values, or whose tensors are not 16-byte aligned, take the loop kernels at
-// the end.
+// is not a multiple of 8 values or above 8192, whose tensors are not 16-byte aligned, or that do not fit
+// shared memory beside the two vectors (the fp32 backward's five arrays above 7896 columns), take the loop
+// kernels at the end.
 // Measured, 8192 x 6144 bf16, gate and both vectors: forward 100 us = 5.0 TB/s (a copy: 6.45), backward 203 us = 4.0
 // TB/s.  The backward is short of warps: its 158 registers a thread (40 of raw values, 32 of column sums, 16 of
 // sigmoids) leave 12 an SM, which issue in 43 % of the cycles and wait for the row's sums in between.  With
 // two syncs a row it took 214 us, with a row a CTA, read again in each pass, 240 (the forward so: 181).
+// 8192 rows in other types, gate and vectors, forward and backward in us (TB/s): fp32 residual, 6144 wide 132 (5.3) and 245
+// (4.5), 8192 wide 198 (4.8) and 392 (3.8); fp32, 4096 wide 132 (5.1) and 243 (4.4), 6144 wide 196 (5.1) and 395 (4.1), 8192
+// wide 317 (4.2) and, in the loop kernel, 1672 (1.3).
 #pragma once
 
 #include "common.cuh"

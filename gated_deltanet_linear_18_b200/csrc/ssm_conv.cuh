@@ -3,14 +3,12 @@
 // with the three rows before the sequence taken from a carried history (zeros without one), and
 // the last three raw rows written out as the history after the call.
 //
-// Each raw row is read once and each result written once; the two special-function calls per value (16 a
-// cycle and SM) take two thirds of that time in bf16, the conversions and sums the rest of the issue
-// slots.  One thread owns VEC neighbouring channels (16 bytes) and a tile of consecutive rows: its taps
+// Each raw row is read once and each result written once.  In bf16 neither the special functions (two a value, 52 % of
+// their pipe) nor the issue slots (60 %) are full: with 16 warps an SM, what is left is latency.  One thread owns VEC neighbouring channels (16 bytes) and a tile of consecutive rows: its taps
 // and the three-row window stay in registers, and the next kConvBatch rows are loaded while the present
 // ones are computed.  A tile is as long as one wave of CTAs allows, since a thread's 5 VEC taps and biases
 // are as many bytes as ten rows of bf16.  Only the window's three rows are read twice.
-// Measured, 16384 x 6144 bf16: 88-90 us = 4.5 TB/s (a copy: 6.45), issuing in 61 % of the cycles; 161 us with
-// tiles of 32 rows.  Rows ahead and CTAs an SM: 2 and 4 95 us, 2 and 5 104, 4 and 5 125, 8 and 3 92; 8-byte
+// Measured, 16384 x 6144: bf16 88-90 us = 4.5 TB/s (a copy: 6.45), 161 with tiles of 32 rows; fp32 175 us = 4.6 TB/s.  Rows ahead and CTAs an SM: 2 and 4 95 us, 2 and 5 104, 4 and 5 125, 8 and 3 92; 8-byte
 // pieces with twice the warps 104; a branch for four rows of one sequence, without the question of each
 // row's sequence, 107 (it spills).
 #pragma once

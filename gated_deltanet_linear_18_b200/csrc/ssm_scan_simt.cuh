@@ -5,10 +5,13 @@
 // A CTA owns PT columns of one (sequence, head): 128 threads as PT columns x NG groups of N / NG state rows,
 // the state in registers.  Tokens come in tiles through shared memory (B and C as rows that a warp
 // reads at few addresses); the next tile is loaded into registers while this one is computed, and the NG
-// partial read-outs of a tile are added at its end.  Bound by the chain of tokens (3 N P operations each,
-// issued by four warps); it is the fp32 path and the one for shapes without a tensor-core kernel.  Measured,
-// 2 x 333 tokens of 6 heads of 16 x 32 with gates: 33 us; 38 with the gate's values loaded when they are
-// needed, 52 with every tile loaded only when its turn came.
+// partial read-outs of a tile are added at its end.  It is the fp32 path and the one for shapes and row distances
+// without a tensor-core kernel.  A CTA walks its sequence token by token, so that few sequences and heads leave most SMs
+// idle (12 CTAs below) and the time is tokens x 0.1 to 0.2 us; the recurrence would allow to cut the tokens into segments as
+// the tensor-core kernel does, which this kernel does not.  Measured, 2 x 333 tokens of 6 heads of 16 x 32 with gates:
+// 35 us through the binding, 33 of the kernel; 38 with the gate's values loaded when they are needed, 52 with every tile
+// loaded only when its turn came.  At model size: 8192 tokens of 64 heads of 128 x 64 with gates, 1.73 ms in fp32 and
+// 1.83 in bf16; of 16 x 64, 0.91 ms in bf16; 4 x 2048 tokens of 48 heads of 128 x 128, 1.50 ms in fp32.
 #pragma once
 
 #include "ssm_common.cuh"

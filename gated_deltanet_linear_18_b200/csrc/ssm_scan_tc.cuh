@@ -12,8 +12,11 @@
 //   Ya [t, hp] = P_h X_h                    (P from TMEM, the raw x tile as the other operand)
 //   U  [hp, n] = X'^T B,  X' = exp(c_L - c_s) D_s x_s as three bf16 terms (24 bits: the fp32 state
 //                         keeps fp32 accuracy; B and x are exact)
-// and y = exp(c_t) Yi + Ya + D x, S' = exp(c_L) S + U in fp32 registers; the state's copy that Yi reads is
-// rounded to bf16 once a chunk, P once.
+// and y = exp(c_t) Yi + Ya + D x, S' = exp(c_L) S + U in fp32 registers.  Two roundings to bf16 are chosen: of the state's
+// copy that Yi reads, once a chunk, and of P, once (2^-8 of each term at most).  They reach y only, never the state, and y is
+// rounded to bf16 itself: its error against fp64 is 1.84e-3 to 1.91e-3 of its norm on the prompts below, 1.66e-3 of which
+// that last rounding makes.  A second term for each, as X' has, would double the MMAs of Yi and Ya and needs 128 columns of
+// TMEM and up to 32 KB of shared memory that the CTA does not have.
 //
 // Decays are never formed as differences of long sums: a chunk is four blocks of 32 tokens (a warp's lanes).
 // c_t - c_s inside a block is the difference of that block's prefix sums, across blocks it is
@@ -29,9 +32,8 @@
 //   warpgroups 3 and 4 form y, 64 columns each, in place of x in its tile, which leaves by a TMA store.
 // B and C, which the heads of a group share, come from L2.
 //
-// The decay vectors (five numbers a token and head) come from a small kernel before: formed here they were a role
-// of 1000 instructions run by one warp, and what bounds this kernel is how fast the SM gets its instructions
-// (about 60 KB of code for all roles; every role that got shorter made the others faster).
+// The decay vectors (five numbers a token and head) come from a small kernel before: formed here they kept one warp busy
+// with 1000 instructions a chunk.
 //
 // One CTA an SM stays and takes one item after another (a sequence's columns, or a segment of them) from a counter;
 // the roles go on into the next item while others finish the last, so that a short sequence costs little more than its
@@ -42,10 +44,13 @@
 // states before it, combined in order (the result does not depend on timing).  That is done for the (sequence,
 // column) pairs that do not fill a wave of the SMs: 192 of them run as 148 whole ones and 44 in three segments.
 //
-// Measured (bf16): 8192 tokens of 64 heads of 128 x 64, gated, 139 us (decays 8, first launch 37, second 97); 4 x 2048
-// tokens of 48 heads of 128 x 128, 112-117 us; a ragged batch of 32 prompts of 64 heads, gated, 160 us.  A chunk takes
-// about 5 us.  352 KB of MMA operands and about as much of tiles pass through shared memory in it (2.9 us at 128 bytes a
-// cycle); the rest is what the roles wait for one another and for instructions.
+// Measured (bf16, inputs that are not in L2): 8192 tokens of 64 heads of 128 x 64, gated, 139-144 us (decays 8, first launch
+// about 37, the rest the second); 4 x 2048 tokens of 48 heads of 128 x 128, 124-129 us (114 with the inputs in L2); a ragged
+// batch of 32 prompts of 64 heads, gated, 157-163 us.  A chunk takes about 5 us.  352 KB of MMA operands and about as much
+// of tiles pass through shared memory in it (2.9 us at 128 bytes a cycle); the rest is what the roles wait for one
+// another.  Counted for 128 x 128: the tensor pipe is active in 40 % of the cycles, the issue slots in 47 %; per issued
+// instruction a warp waits 4.7 cycles for loads, barriers and TMEM (long scoreboard), 1.2 for shared memory and 0.5 for
+// instructions.  The kernels with outputs and N = 128 spill 160 bytes.
 #pragma once
 
 #include <cuda.h>
@@ -982,7 +987,8 @@ inline int columns(int H, int G, int P) {       // CTAs of one sequence and segm
 // How the pairs are cut, a rule on sizes alone (so that the workspace can be sized without a device).  Of n pairs
 // floor(n / 148) full waves run whole; the rest r is cut into as many segments as fill one more wave, none shorter than
 // four chunks (a segment costs the first launch and the combination, about two chunks' time).  4 x 48 pairs of 16
-// chunks: 132 us whole in two waves, of which the second has 44 CTAs, and 123 cut (114 by now).  From five waves on nothing is cut.
+// chunks (inputs in L2): 132 us whole in two waves, of which the second has 44 CTAs, and 123 cut when that was compared; 114
+// now.  From five waves on nothing is cut.
 struct Cut {
   int whole, segments;
 };
