@@ -48,8 +48,8 @@
 // about 37, the rest the second); 4 x 2048 tokens of 48 heads of 128 x 128, 124-129 us (114 with the inputs in L2); a ragged
 // batch of 32 prompts of 64 heads, gated, 157-163 us.  A chunk takes about 5 us.  352 KB of MMA operands and about as much
 // of tiles pass through shared memory in it (2.9 us at 128 bytes a cycle); the rest is what the roles wait for one
-// another.  Counted for 128 x 128: the tensor pipe is active in 40 % of the cycles, the issue slots in 47 %; per issued
-// instruction a warp waits 4.7 cycles for loads, barriers and TMEM (long scoreboard), 1.2 for shared memory and 0.5 for
+// another.  Counted for 128 x 128: the tensor pipe is active in 39 % of the cycles, the issue slots in 47 %; per issued
+// instruction a warp waits 4.7 cycles for loads, barriers and TMEM (long scoreboard), 1.3 for shared memory and 0.6 for
 // instructions.  The kernels with outputs and N = 128 spill 160 bytes.
 #pragma once
 
