@@ -847,6 +847,7 @@ def ssm_conv_varlen(x, w, bias, cu_seqlens, max_seqlen: int, *, hist=None, want_
 def ssm_scan_workspace_bytes(nseq, max_seqlen, H, G, P, N, dtype, total: Optional[int] = None) -> int:
     """Device scratch bytes ``ssm_scan`` / ``ssm_scan_varlen`` need (0: none); with ``total``, the rows of
     a packed call, no more than its rows make necessary."""
+    _fit(nseq, max_seqlen, H, G, P, N, total or 0)
     if total is not None:
         return int(lib().gdn_ssm_scan_varlen_workspace_bytes(nseq, max_seqlen, total, H, G, P, N, _DTYPES[dtype]))
     return int(lib().gdn_ssm_scan_workspace_bytes(nseq, max_seqlen, H, G, P, N, _DTYPES[dtype]))
@@ -1002,6 +1003,7 @@ def block_norm(y, h, *, w_post=None, w_pre=None, z=None, res_scale=None, eps: fl
 
 def block_norm_bwd_workspace_bytes(rows: int, D: int) -> int:
     """Device scratch bytes one ``block_norm_bwd`` call needs."""
+    _fit(D)
     return int(lib().gdn_block_norm_bwd_workspace_bytes(rows, D))
 
 

@@ -31,6 +31,9 @@ CALLS = {
     "scan rows": lambda: gdn.ssm_scan(t(1, BIG, 1, 16), t(1, BIG, 1), f(1), t(1, BIG, 1, 16), t(1, BIG, 1, 16)),
     "packed scan rows": lambda: gdn.ssm_scan_varlen(t(BIG, 1, 16), t(BIG, 1), f(1), t(BIG, 1, 16), t(BIG, 1, 16), CU, 8),
     "packed scan bound": lambda: gdn.ssm_scan_varlen(t(8, 1, 16), t(8, 1), f(1), t(8, 1, 16), t(8, 1, 16), CU, 2 ** 32),
+    "scan scratch": lambda: gdn.ssm_scan_workspace_bytes(3, 2 ** 32, 2, 1, 64, 64, torch.bfloat16),
+    "packed scan scratch": lambda: gdn.ssm_scan_workspace_bytes(3, 8, 2, 1, 64, 64, torch.bfloat16, total=2 ** 32),
+    "norm scratch": lambda: gdn.block_norm_bwd_workspace_bytes(4, BIG),
     "norm width": lambda: gdn.block_norm(t(1, BIG), t(1, BIG)),
     "norm backward width": lambda: gdn.block_norm_bwd(t(1, BIG), t(1, BIG), t(1, BIG)),
 }
