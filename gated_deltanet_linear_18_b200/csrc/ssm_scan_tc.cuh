@@ -44,9 +44,9 @@
 // states before it, combined in order (the result does not depend on timing).  That is done for the (sequence,
 // column) pairs that do not fill a wave of the SMs: 192 of them run as 148 whole ones and 44 in three segments.
 //
-// Measured (bf16, inputs that are not in L2): 8192 tokens of 64 heads of 128 x 64, gated, 139-144 us (decays 8, first launch
-// about 37, the rest the second); 4 x 2048 tokens of 48 heads of 128 x 128, 124-129 us (114 with the inputs in L2); a ragged
-// batch of 32 prompts of 64 heads, gated, 157-163 us.  A chunk takes about 5 us.  352 KB of MMA operands and about as much
+// Measured (bf16, inputs that are not in L2): 8192 tokens of 64 heads of 128 x 64, gated, 139-147 us (decays 8, first launch
+// about 37, the rest the second); 4 x 2048 tokens of 48 heads of 128 x 128, 124-131 us (114 with the inputs in L2); a ragged
+// batch of 32 prompts of 64 heads, gated, 157-164 us.  A chunk takes about 5 us.  352 KB of MMA operands and about as much
 // of tiles pass through shared memory in it (2.9 us at 128 bytes a cycle); the rest is what the roles wait for one
 // another.  Counted for 128 x 128: the tensor pipe is active in 39 % of the cycles, the issue slots in 47 %; per issued
 // instruction a warp waits 4.7 cycles for loads, barriers and TMEM (long scoreboard), 1.3 for shared memory and 0.6 for
